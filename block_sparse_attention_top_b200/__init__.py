@@ -17,9 +17,19 @@ workspace with torch.
     o = bsa.sparse_attn(plan, q, k, v, row_ptr, col_idx)        # bf16 [B, N, H, d]
     o8 = bsa.sparse_attn_fp8v(plan, q, k, v, row_ptr, col_idx)  # e4m3 P.V product
     assert bsa.bsa_last_device_error(plan) == bsa.BSA_OK
+
+The operators of a block around its self-attention (cross attention to an
+encoder's states, and the norms with modulation, gate and residual) take the
+same plan; `dit_block` runs a whole block:
+
+    c = bsa.cross_attn(plan, q, k_text, v_text, kv_len=lengths)       # k, v: bf16 [B, M, Hkv, d]
+    h = bsa.norm_modulate(plan, x, scale=s1, shift=t1)                 # x: [B, N, C] bf16 or float32
+    x, h = bsa.residual_norm(plan, x, y, gate=g1, scale=s2, shift=t2)  # x + g1 y, then its norm
+    # gradients: cross_attn_backward, norm_modulate_backward, residual_norm_backward
 """
 from __future__ import annotations
 
+import collections
 import ctypes
 import os
 
@@ -41,11 +51,22 @@ BSA_ORDER_HILBERT2D_FRAME, BSA_ORDER_IDENTITY = 0, 1
 BSA_BF16, BSA_F32 = 0, 1
 BSA_OP_ROUTE, BSA_OP_ATTN, BSA_OP_MASK, BSA_OP_AUGMENT = 0, 1, 2, 3
 BSA_SCHED_L2_HEADS, BSA_SCHED_HEAVIEST_FIRST, BSA_SCHED_IN_ORDER = 0, 1, 2
+BSA_NORM_NONE, BSA_NORM_LAYER, BSA_NORM_RMS = 0, 1, 2
 
 _P = ctypes.c_void_p
 _I = ctypes.c_int
 _I64 = ctypes.c_int64
 _SZ = ctypes.c_size_t
+
+
+class NormArgs(ctypes.Structure):
+    """bsa_norm_args."""
+    _fields_ = [("C", _I), ("groups", _I), ("dtype", _I), ("norm", _I), ("post_norm", _I),
+                ("eps", ctypes.c_float), ("res_scale", ctypes.c_float), ("gate", _P), ("scale", _P), ("shift", _P),
+                ("weight", _P), ("bias", _P), ("post_weight", _P)]
+
+
+_NA = ctypes.POINTER(NormArgs)
 
 _SIGS = {
     "bsa_plan_create": (_I, [ctypes.POINTER(_P), _I, _I, _I, _I, _I, _I, _I, _I]),
@@ -79,6 +100,14 @@ _SIGS = {
     "bsa_sparse_attn_fp8v": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]),
     "bsa_attn_prepare_fp8v": (_I, [_P, _P, _P, _P, _P, _P, _SZ, _P]),
     "bsa_attn_run_fp8v": (_I, [_P, _P, _P, _P, _P, _SZ, _P]),
+    "bsa_cross_attn": (_I, [_P, _P, _P, _P, _I64, _I, _P, _P, _P, _P, _P, _P, _SZ, _P]),
+    "bsa_cross_attn_bwd": (_I, [_P, _P, _P, _P, _I64, _I, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]),
+    "bsa_cross_attn_workspace_size": (_SZ, [_P, _I64, _I, _I]),
+    "bsa_norm_modulate": (_I, [_P, _NA, _P, _P, _P]),
+    "bsa_residual_norm": (_I, [_P, _NA, _P, _P, _P, _P, _P]),
+    "bsa_norm_modulate_bwd": (_I, [_P, _NA, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]),
+    "bsa_residual_norm_bwd": (_I, [_P, _NA, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]),
+    "bsa_norm_bwd_workspace_size": (_SZ, [_P, _NA]),
     "bsa_last_device_error": (_I, [_P, _P]),
     "bsa_strerror": (ctypes.c_char_p, [_I]),
 }
@@ -130,6 +159,7 @@ class Plan:
         n, nb, rows = _I64(), _I64(), _I64()
         _check(_lib.bsa_plan_info(h, ctypes.byref(n), ctypes.byref(nb), ctypes.byref(rows)), "bsa_plan_info")
         self.N, self.nb, self.rows = n.value, nb.value, rows.value
+        self.device = torch.device("cuda", torch.cuda.current_device())
 
     def set_schedule(self, schedule: int) -> None:
         _check(_lib.bsa_plan_set_schedule(self.handle, int(schedule)), "bsa_plan_set_schedule")
@@ -540,3 +570,232 @@ def sparse_attn_fp8v(plan: Plan, q, k, v, row_ptr, col_idx, workspace=None, out=
     o = torch.empty_like(q) if out is None else out
     _check(bsa_sparse_attn_fp8v(plan, q, k, v, row_ptr, col_idx, o, workspace, stream), "bsa_sparse_attn_fp8v")
     return o
+
+
+# ---- operators of a block around its self-attention ----
+#
+# These check types, shapes, layouts and devices (ValueError) before the call; the library checks the rest
+# (BsaError).  Outputs and workspace come from `stream`'s pool (default: the current stream), so nothing
+# that a launch still uses is handed out again.
+
+class _On:
+    """Makes `stream` (None: the current one) the current stream of the plan's device, and that device current."""
+
+    def __init__(self, plan, stream):
+        if stream is not None and not isinstance(stream, torch.cuda.Stream):
+            raw = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+            stream = torch.cuda.ExternalStream(raw, device=plan.device)
+        if stream is not None and stream.device != plan.device:
+            raise ValueError(f"stream is on {stream.device}, the plan on {plan.device}")
+        self._dev, self._stream = torch.cuda.device(plan.device), torch.cuda.stream(stream)
+
+    def __enter__(self):
+        self._dev.__enter__()
+        self._stream.__enter__()
+        return torch.cuda.current_stream().cuda_stream
+
+    def __exit__(self, *exc):
+        self._stream.__exit__(*exc)
+        self._dev.__exit__(*exc)
+
+
+def _need(plan, t, name, dtypes, shape, dense=True):
+    if not isinstance(t, torch.Tensor) or t.device != plan.device:
+        raise ValueError(f"{name} must be a tensor on {plan.device}")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, not {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {list(shape)}, not {list(t.shape)}")
+    if dense and not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _workspace(plan, need, workspace):
+    if workspace is None:
+        return torch.empty(need, dtype=torch.uint8, device=plan.device) if need else None
+    _need(plan, workspace, "workspace", (torch.uint8,), workspace.shape)
+    return workspace
+
+
+_BF16 = (torch.bfloat16,)
+
+
+def _cross_inputs(plan, q, k, v, kv_len, key_mask):
+    """Checks and the strides array of a cross attention's inputs: (M, Hkv, strides)."""
+    _need(plan, q, "q", _BF16, (plan.B, plan.N, plan.H, plan.d), dense=False)
+    if not isinstance(k, torch.Tensor) or k.dim() != 4:
+        raise ValueError("k must be [B, M, Hkv, d]")
+    M, Hkv = k.shape[1], k.shape[2]
+    _need(plan, k, "k", _BF16, (plan.B, M, Hkv, plan.d), dense=False)
+    _need(plan, v, "v", _BF16, (plan.B, M, Hkv, plan.d), dense=False)
+    for t, name in ((q, "q"), (k, "k"), (v, "v")):
+        if t.stride(3) != 1:
+            raise ValueError(f"the channels of {name} must be contiguous")
+    if kv_len is not None:
+        _need(plan, kv_len, "kv_len", (torch.int32,), (plan.B,))
+    if key_mask is not None:
+        _need(plan, key_mask, "key_mask", (torch.bool, torch.uint8), (plan.B, M))
+    return M, Hkv, (_I64 * 9)(*(t.stride(i) for t in (q, k, v) for i in range(3)))
+
+
+def cross_attn(plan: Plan, q, k, v, kv_len=None, key_mask=None, return_lse=False, workspace=None, out=None,
+               stream=None):
+    """Cross attention of the plan's query tokens to an encoder's states (bsa_cross_attn).
+
+    q: bf16 [B,N,H,d]; k, v: bf16 [B,M,Hkv,d], Hkv dividing H, e.g. views into one projection (channels
+    contiguous, other strides multiples of 8 elements).  kv_len: int32 [B] on the device, key_mask: bool
+    [B,M]; a state counts when both say so.  Returns o bf16 [B,N,H,d], or (o, lse float32 [B,H,N])."""
+    M, Hkv, strides = _cross_inputs(plan, q, k, v, kv_len, key_mask)
+    if out is not None:
+        _need(plan, out, "out", _BF16, q.shape)
+    with _On(plan, stream) as s:
+        o = torch.empty(q.shape, dtype=q.dtype, device=plan.device) if out is None else out
+        lse = torch.empty(plan.B, plan.H, plan.N, dtype=torch.float32, device=plan.device) if return_lse else None
+        ws = _workspace(plan, _lib.bsa_cross_attn_workspace_size(plan.handle, M, Hkv, 0), workspace)
+        _check(_lib.bsa_cross_attn(plan.handle, _ptr(q), _ptr(k), _ptr(v), M, Hkv, strides, _ptr(kv_len),
+                                   _ptr(key_mask), _ptr(o), _ptr(lse), _ptr(ws), ws.numel() if ws is not None else 0,
+                                   s), "bsa_cross_attn")
+    return (o, lse) if return_lse else o
+
+
+def cross_attn_backward(plan: Plan, do, q, k, v, o, lse, kv_len=None, key_mask=None, workspace=None, stream=None):
+    """Gradients (dq, dk, dv) of cross_attn from do, its inputs and its outputs (bsa_cross_attn_bwd)."""
+    M, Hkv, strides = _cross_inputs(plan, q, k, v, kv_len, key_mask)
+    _need(plan, do, "do", _BF16, q.shape)
+    _need(plan, o, "o", _BF16, q.shape)
+    _need(plan, lse, "lse", (torch.float32,), (plan.B, plan.H, plan.N))
+    with _On(plan, stream) as s:
+        dq = torch.empty(q.shape, dtype=q.dtype, device=plan.device)
+        dk = torch.empty(k.shape, dtype=k.dtype, device=plan.device)
+        dv = torch.empty(v.shape, dtype=v.dtype, device=plan.device)
+        ws = _workspace(plan, _lib.bsa_cross_attn_workspace_size(plan.handle, M, Hkv, 1), workspace)
+        _check(_lib.bsa_cross_attn_bwd(plan.handle, _ptr(q), _ptr(k), _ptr(v), M, Hkv, strides, _ptr(kv_len),
+                                       _ptr(key_mask), _ptr(o), _ptr(lse), _ptr(do), _ptr(dq), _ptr(dk), _ptr(dv),
+                                       _ptr(ws), ws.numel() if ws is not None else 0, s), "bsa_cross_attn_bwd")
+    return dq, dk, dv
+
+
+def _norm_inputs(plan, x, gate, scale, shift, weight, bias, post_weight, norm, post_norm, res_scale, eps):
+    """Checks of a norm operator's stream and parameters, as a filled NormArgs."""
+    if not isinstance(x, torch.Tensor) or x.dim() != 3:
+        raise ValueError("x must be [B, N, C]")
+    C = x.shape[2]
+    _need(plan, x, "x", (torch.bfloat16, torch.float32), (plan.B, plan.N, C))
+    groups = 1
+    for t, name in ((gate, "gate"), (scale, "scale"), (shift, "shift")):
+        if t is None:
+            continue
+        if not isinstance(t, torch.Tensor) or t.dim() != 3:
+            raise ValueError(f"{name} must be [B, groups, C]")
+        if groups != 1 and t.shape[1] != groups:
+            raise ValueError("gate, scale and shift must have the same number of groups")
+        groups = t.shape[1]
+    for t, name in ((gate, "gate"), (scale, "scale"), (shift, "shift")):
+        if t is not None:
+            _need(plan, t, name, (torch.float32,), (plan.B, groups, C))
+    for t, name in ((weight, "weight"), (bias, "bias"), (post_weight, "post_weight")):
+        if t is not None:
+            _need(plan, t, name, (torch.float32,), (C,))
+    return NormArgs(C, groups, BSA_BF16 if x.dtype == torch.bfloat16 else BSA_F32, norm, post_norm, eps, res_scale,
+                    _ptr(gate), _ptr(scale), _ptr(shift), _ptr(weight), _ptr(bias), _ptr(post_weight))
+
+
+def norm_modulate(plan: Plan, x, scale=None, shift=None, weight=None, bias=None, norm=BSA_NORM_LAYER, eps=1e-6,
+                  out=None, stream=None):
+    """h = (norm(x) * weight + bias) * (1 + scale) + shift in bf16 (bsa_norm_modulate).  x: bf16 or float32
+    [B,N,C]; scale, shift: float32 [B,groups,C], token n in group n // (N / groups); weight, bias: float32 [C]."""
+    a = _norm_inputs(plan, x, None, scale, shift, weight, bias, None, norm, BSA_NORM_NONE, 1.0, eps)
+    if out is not None:
+        _need(plan, out, "out", _BF16, x.shape)
+    with _On(plan, stream) as s:
+        h = torch.empty(x.shape, dtype=torch.bfloat16, device=plan.device) if out is None else out
+        _check(_lib.bsa_norm_modulate(plan.handle, ctypes.byref(a), _ptr(x), _ptr(h), s), "bsa_norm_modulate")
+    return h
+
+
+def residual_norm(plan: Plan, x, y, gate=None, scale=None, shift=None, weight=None, bias=None, post_weight=None,
+                  norm=BSA_NORM_LAYER, post_norm=BSA_NORM_NONE, res_scale=1.0, eps=1e-6, x_out=None, h_out=None,
+                  stream=None):
+    """A block's boundary (bsa_residual_norm): x_out = res_scale x + gate (post_norm(y) post_weight) in x's type and
+    h = (norm(x_out) weight + bias)(1 + scale) + shift in bf16.  y: bf16 [B,N,C]; parameters as for
+    norm_modulate.  norm=BSA_NORM_NONE: no h.  x_out may be x, h_out may be y.  Returns (x_out, h or None)."""
+    a = _norm_inputs(plan, x, gate, scale, shift, weight, bias, post_weight, norm, post_norm, res_scale, eps)
+    _need(plan, y, "y", _BF16, x.shape)
+    if x_out is not None:
+        _need(plan, x_out, "x_out", (x.dtype,), x.shape)
+    if h_out is not None:
+        _need(plan, h_out, "h_out", _BF16, x.shape)
+    with _On(plan, stream) as s:
+        xo = torch.empty_like(x) if x_out is None else x_out
+        h = None
+        if norm != BSA_NORM_NONE:
+            h = torch.empty_like(y) if h_out is None else h_out
+        _check(_lib.bsa_residual_norm(plan.handle, ctypes.byref(a), _ptr(x), _ptr(y), _ptr(xo), _ptr(h), s),
+               "bsa_residual_norm")
+    return xo, h
+
+
+NormGrads = collections.namedtuple("NormGrads", "dx dy dgate dscale dshift dweight dbias dpost_weight")
+
+
+def _like(t):
+    return None if t is None else torch.empty_like(t)
+
+
+def norm_modulate_backward(plan: Plan, dh, x, scale=None, shift=None, weight=None, bias=None, norm=BSA_NORM_LAYER,
+                           eps=1e-6, workspace=None, stream=None):
+    """Gradients of norm_modulate from dh (bf16) as NormGrads: dx in x's type, one float32 tensor for each
+    parameter given, None for the rest (bsa_norm_modulate_bwd)."""
+    a = _norm_inputs(plan, x, None, scale, shift, weight, bias, None, norm, BSA_NORM_NONE, 1.0, eps)
+    _need(plan, dh, "dh", _BF16, x.shape)
+    with _On(plan, stream) as s:
+        dx, ds, dt, dw, db = (_like(t) for t in (x, scale, shift, weight, bias))
+        ws = _workspace(plan, _lib.bsa_norm_bwd_workspace_size(plan.handle, ctypes.byref(a)), workspace)
+        _check(_lib.bsa_norm_modulate_bwd(plan.handle, ctypes.byref(a), _ptr(dh), _ptr(x), _ptr(dx), _ptr(ds),
+                                          _ptr(dt), _ptr(dw), _ptr(db), _ptr(ws), ws.numel() if ws is not None else 0,
+                                          s), "bsa_norm_modulate_bwd")
+    return NormGrads(dx, None, None, ds, dt, dw, db, None)
+
+
+def residual_norm_backward(plan: Plan, dh, dx_out, x_out, y, gate=None, scale=None, shift=None, weight=None,
+                           bias=None, post_weight=None, norm=BSA_NORM_LAYER, post_norm=BSA_NORM_NONE, res_scale=1.0,
+                           eps=1e-6, workspace=None, stream=None):
+    """Gradients of residual_norm (bsa_residual_norm_bwd) from those of its outputs: dh (bf16; None exactly when
+    norm is BSA_NORM_NONE) and dx_out (x's type, or None for zero).  x_out: the forward pass's output, y its
+    input.  Returns NormGrads: dx, dy, and one float32 tensor for each parameter given."""
+    a = _norm_inputs(plan, x_out, gate, scale, shift, weight, bias, post_weight, norm, post_norm, res_scale, eps)
+    _need(plan, y, "y", _BF16, x_out.shape)
+    if dh is not None:
+        _need(plan, dh, "dh", _BF16, x_out.shape)
+    if dx_out is not None:
+        _need(plan, dx_out, "dx_out", (x_out.dtype,), x_out.shape)
+    with _On(plan, stream) as s:
+        dx, dy, dg, ds, dt, dw, db, dp = (_like(t) for t in (x_out, y, gate, scale, shift, weight, bias, post_weight))
+        ws = _workspace(plan, _lib.bsa_norm_bwd_workspace_size(plan.handle, ctypes.byref(a)), workspace)
+        _check(_lib.bsa_residual_norm_bwd(plan.handle, ctypes.byref(a), _ptr(dh), _ptr(dx_out), _ptr(x_out), _ptr(y),
+                                          _ptr(dx), _ptr(dy), _ptr(dg), _ptr(ds), _ptr(dt), _ptr(dw), _ptr(db),
+                                          _ptr(dp), _ptr(ws), ws.numel() if ws is not None else 0, s),
+               "bsa_residual_norm_bwd")
+    return NormGrads(dx, dy, dg, ds, dt, dw, db, dp)
+
+
+def dit_block(plan: Plan, x, mod, qkv, attn_out, cross_q, cross_out, ffn, k_ctx, v_ctx, p, k_floor, kv_len=None,
+              key_mask=None, cross_weight=None, cross_bias=None, norm=BSA_NORM_LAYER, eps=1e-6):
+    """One video transformer block: routed block-sparse self-attention, cross attention to an encoder's states
+    and the feed-forward half, each between its norms.
+
+    x: [B,N,C] bf16 or float32; mod: six float32 [B,groups,C] tensors (shift, scale, gate of the self-attention
+    half, then of the feed-forward half).  The host model's projections are callables: qkv(h) -> three [B,N,H,d],
+    attn_out(o) -> y, cross_q(h) -> [B,N,H,d], cross_out(o) -> y, ffn(h) -> y, with h and y bf16 [B,N,C].
+    k_ctx, v_ctx: bf16 [B,M,Hkv,d] projections of the encoder's states; kv_len, key_mask: as for cross_attn;
+    cross_weight, cross_bias: affine of the norm before the cross attention.  p, k_floor: as for route.
+    Returns the block's output in x's type."""
+    t1, s1, g1, t2, s2, g2 = mod
+    h = norm_modulate(plan, x, scale=s1, shift=t1, norm=norm, eps=eps)
+    q, k, v = qkv(h)
+    row_ptr, col_idx, _, _ = route(plan, q, k, p, k_floor)
+    y = attn_out(sparse_attn(plan, q, k, v, row_ptr, col_idx))
+    x, h = residual_norm(plan, x, y, gate=g1, weight=cross_weight, bias=cross_bias, norm=norm, eps=eps)
+    y = cross_out(cross_attn(plan, cross_q(h), k_ctx, v_ctx, kv_len=kv_len, key_mask=key_mask))
+    x, h = residual_norm(plan, x, y, scale=s2, shift=t2, norm=norm, eps=eps)
+    return residual_norm(plan, x, ffn(h), gate=g2, norm=BSA_NORM_NONE, eps=eps)[0]

@@ -112,6 +112,30 @@ cudaError_t launch_attn_pp(const bsa_plan& p, const void* qp, const void* kp, co
 // e4m3 V: sigma [B*H*d] floats (per head and channel), vt [B*H*nb*d, 128] bytes
 cudaError_t launch_quant_v(const bsa_plan& p, const void* v, float* sigma, void* vt, cudaStream_t s);
 
+// ---- block operators: cross attention and the norms (cross.cu, norm.cu) ----
+struct CrossArgs {
+    const void *q, *k, *v;
+    int64_t M;
+    int Hkv;
+    int64_t st[9];               // batch, token, head strides of q, k, v in elements
+    const int32_t* kv_len;       // [B] or null
+    const uint8_t* key_mask;     // [B, M] or null
+};
+size_t cross_ws_bytes(const bsa_plan& p, int64_t M, int Hkv, bool backward);
+cudaError_t launch_cross(const bsa_plan& p, const CrossArgs& a, void* o, float* lse, void* ws, cudaStream_t s);
+cudaError_t launch_cross_bwd(const bsa_plan& p, const CrossArgs& a, const void* o, const float* lse, const void* d_o,
+                             void* dq, void* dk, void* dv, void* ws, cudaStream_t s);
+struct NormGrads {
+    float *dgate, *dscale, *dshift, *dweight, *dbias, *dpost_weight;
+};
+// y null: no residual sum (bsa_norm_modulate)
+cudaError_t launch_norm(const bsa_plan& p, const bsa_norm_args& a, const void* x, const void* y, void* x_out, void* h,
+                        cudaStream_t s);
+size_t norm_bwd_ws_bytes(const bsa_plan& p, const bsa_norm_args& a);
+cudaError_t launch_norm_bwd(const bsa_plan& p, const bsa_norm_args& a, const NormGrads& out, const void* dh,
+                            const void* dx_out, const void* x_out, const void* y, void* dx, void* dy, void* ws,
+                            cudaStream_t s);
+
 // Host-side token order (no CUDA).
 void token_order(int T, int Hs, int Ws, int order, int32_t* perm);
 

@@ -432,6 +432,140 @@ int bsa_attn_intermediates(const bsa_plan* plan, void* workspace, const int32_t*
 int bsa_attn_run_simt(const bsa_plan* plan, const int32_t* row_ptr, const int32_t* col_idx,
                       void* o, void* workspace, size_t ws_bytes, void* stream);
 
+/* ---- norms of the block operators ---- */
+#define BSA_NORM_NONE  0
+#define BSA_NORM_LAYER 1   /* (x - mean) / sqrt(var + eps), biased variance */
+#define BSA_NORM_RMS   2   /* x / sqrt(mean(x^2) + eps) */
+
+/*
+ * ------------------------------------------------------------------------
+ * Operators of a video transformer block around its self-attention: cross
+ * attention to an encoder's states, and the norms at the block's boundaries.
+ * The pages leave them to the host model; they take the plan of the
+ * self-attention they stand next to (its B, N, H, head_dim, device, error
+ * word and wait limit; its block size and token order play no part, raster
+ * order in and out).  The plan's device must be current (BSA_EINVAL).
+ * ------------------------------------------------------------------------
+ */
+
+/*
+ * Cross attention of the plan's N query tokens to M states of an encoder:
+ *   O[b, n, h, :] = sum_j softmax_j(Q[b,n,h,:] . K[b,j,g,:] / sqrt(d)) V[b,j,g,:],
+ *   g = h / (H / Hkv), j over the valid states of batch entry b.
+ * A query row without any valid state (M = 0, kv_len 0, an all-zero mask)
+ * gives zeros and lse = -inf.
+ * q: bf16 [B,N,H,d]; k, v: bf16 [B,M,Hkv,d], Hkv divides H.
+ * strides: NULL (all three dense), or HOST int64 [9]: the batch, token and
+ *   head strides of q, then k, then v, in elements; the d channels of a head
+ *   are contiguous.  Multiples of 8, positive wherever the extent exceeds 1,
+ *   and of at most 2^39 elements (BSA_EUNSUPPORTED otherwise).
+ * kv_len: device int32 [B] or NULL: state j counts when j < kv_len[b] (values
+ *   outside [0, M] act as the nearer bound).  key_mask: device uint8 [B,M] or
+ *   NULL: state j counts when its byte is not 0.  Both: a state counts when
+ *   both say so.  States that do not count are never part of a result, even
+ *   where K or V hold infinities or NaN.
+ * o: bf16 [B,N,H,d], dense.  lse: NULL or float [B,H,N], the natural
+ *   logarithm of each row's sum of exponentials (input of the backward pass).
+ * workspace: >= bsa_cross_attn_workspace_size(plan, M, Hkv, 0) bytes,
+ *   256-aligned (NULL when that is 0); nothing in it is kept between calls.
+ * Scores, softmax statistics and sums are fp32; the probabilities enter the
+ * product with V in bf16, as in bsa_sparse_attn.
+ */
+int bsa_cross_attn(const bsa_plan* plan, const void* q, const void* k, const void* v, int64_t M, int Hkv,
+                   const int64_t* strides, const int32_t* kv_len, const uint8_t* key_mask, void* o, float* lse,
+                   void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * Gradient of bsa_cross_attn.  With P = exp(S - lse), S the scaled scores:
+ *   D = rowsum(dO * O), dS = P * (dO V^T - D),
+ *   dV = sum P^T dO, dQ = dS K / sqrt(d), dK = sum dS^T Q / sqrt(d),
+ * the sums over the query tokens and over the query heads that share a key
+ * head.  q, k, v, M, Hkv, strides, kv_len, key_mask: as in the forward call;
+ * o, lse: its outputs; d_o: bf16 [B,N,H,d] dense.  dq [B,N,H,d], dk, dv
+ * [B,M,Hkv,d]: bf16, dense; states that do not count get zero gradients, and
+ * so do query rows without a valid state.  P and dS enter the products in
+ * bf16, sums are fp32, and the result does not depend on scheduling: the
+ * same inputs give the same bits.
+ * workspace: >= bsa_cross_attn_workspace_size(plan, M, Hkv, 1) bytes, 256-aligned.
+ */
+int bsa_cross_attn_bwd(const bsa_plan* plan, const void* q, const void* k, const void* v, int64_t M, int Hkv,
+                       const int64_t* strides, const int32_t* kv_len, const uint8_t* key_mask, const void* o,
+                       const float* lse, const void* d_o, void* dq, void* dk, void* dv, void* workspace,
+                       size_t ws_bytes, void* stream);
+
+/* Device workspace of bsa_cross_attn (backward = 0) or bsa_cross_attn_bwd
+ * (1) in bytes; 0 also for invalid arguments. */
+size_t bsa_cross_attn_workspace_size(const bsa_plan* plan, int64_t M, int Hkv, int backward);
+
+/*
+ * Shape, options and parameters of the norm operators.  Parameters are
+ * device float32 arrays, any of them NULL: gate, scale, shift [B, groups, C]
+ * (token n uses group n / (N / groups): 1 = per batch entry, T = per latent
+ * frame, N = per token); weight, bias, post_weight [C].
+ */
+typedef struct bsa_norm_args {
+    int C;              /* channels, 1 .. 16384 */
+    int groups;         /* divides N */
+    int dtype;          /* of the residual stream x: BSA_BF16 or BSA_F32 */
+    int norm;           /* BSA_NORM_*: the norm that makes h (NONE: no h) */
+    int post_norm;      /* BSA_NORM_*: the norm of the branch y */
+    float eps;          /* > 0 */
+    float res_scale;    /* factor of x in the residual sum */
+    const float* gate;
+    const float* scale;
+    const float* shift;
+    const float* weight;
+    const float* bias;
+    const float* post_weight;
+} bsa_norm_args;
+
+/*
+ * h = (norm(x) * weight + bias) * (1 + scale) + shift, rows of C channels.
+ * x: [B,N,C] of args->dtype; h: bf16 [B,N,C].  gate, post_weight and
+ * res_scale are not read; post_norm must be BSA_NORM_NONE and norm not.
+ */
+int bsa_norm_modulate(const bsa_plan* plan, const bsa_norm_args* args, const void* x, void* h, void* stream);
+
+/*
+ * The boundary between two halves of a block:
+ *   x_out = res_scale * x + gate * (post_norm(y) * post_weight),
+ *   h     = (norm(x_out) * weight + bias) * (1 + scale) + shift.
+ * x, x_out: [B,N,C] of args->dtype; y, h: bf16 [B,N,C].  h is NULL exactly
+ * when args->norm is BSA_NORM_NONE.  h is taken from the fp32 sum, before
+ * x_out is rounded.  x_out may be x and h may be y; no other overlap.
+ */
+int bsa_residual_norm(const bsa_plan* plan, const bsa_norm_args* args, const void* x, const void* y, void* x_out,
+                      void* h, void* stream);
+
+/*
+ * Gradient of bsa_norm_modulate: dx [B,N,C] of args->dtype, and, each unless
+ * NULL, dscale, dshift float [B,groups,C], dweight, dbias float [C].  dh: bf16.
+ * Sums over tokens are fp32 in a fixed order (the same inputs give the same
+ * bits).  workspace: >= bsa_norm_bwd_workspace_size bytes, 256-aligned.
+ */
+int bsa_norm_modulate_bwd(const bsa_plan* plan, const bsa_norm_args* args, const void* dh, const void* x, void* dx,
+                          float* dscale, float* dshift, float* dweight, float* dbias, void* workspace,
+                          size_t ws_bytes, void* stream);
+
+/*
+ * Gradient of bsa_residual_norm from the gradients of both its outputs, dh
+ * (bf16; NULL exactly when args->norm is BSA_NORM_NONE) and dx_out
+ * ([B,N,C] of args->dtype, or NULL for zero; not both NULL).  x_out: the
+ * forward pass's output; y: its input.  With g the total gradient of x_out:
+ *   dx = res_scale * g (args->dtype), dy (bf16) = gate * g taken through
+ *   post_norm, dgate, dscale, dshift float [B,groups,C], dweight, dbias,
+ *   dpost_weight float [C]; each of the six unless NULL.
+ * dx may be dx_out and dy may be y; no other overlap.  Workspace and order
+ * of sums as for bsa_norm_modulate_bwd.
+ */
+int bsa_residual_norm_bwd(const bsa_plan* plan, const bsa_norm_args* args, const void* dh, const void* dx_out,
+                          const void* x_out, const void* y, void* dx, void* dy, float* dgate, float* dscale,
+                          float* dshift, float* dweight, float* dbias, float* dpost_weight, void* workspace,
+                          size_t ws_bytes, void* stream);
+
+/* Device workspace of the two norm gradients in bytes; 0 also for invalid arguments. */
+size_t bsa_norm_bwd_workspace_size(const bsa_plan* plan, const bsa_norm_args* args);
+
 /*
  * Synchronise `stream`, then read and clear the plan's device error word.
  * Returns BSA_OK, or the first device-side status recorded since the last
