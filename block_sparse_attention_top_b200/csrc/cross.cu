@@ -2,7 +2,7 @@
 // one warp per query row or key, fp32 throughout.
 #include <cuda_bf16.h>
 
-#include "bsa_internal.cuh"
+#include "cross_common.cuh"
 
 namespace bsa {
 namespace {
@@ -165,6 +165,7 @@ size_t cross_ws_bytes(const bsa_plan& p, int64_t M, int Hkv, bool backward) {
 }
 
 cudaError_t launch_cross(const bsa_plan& p, const CrossArgs& a, void* o, float* lse, void*, cudaStream_t s) {
+    if (a.M > 0) return launch_cross_fwd_tc(p, a, o, lse, s);
     const CrossP c = cross_params(p, a);
     auto kern = p.d == 128 ? k_cross_rows<128> : k_cross_rows<64>;
     kern<<<row_grid(p.B * p.N * p.H), 32 * kRowWarps, 0, s>>>(c, (__nv_bfloat16*)o, lse);

@@ -1,0 +1,86 @@
+// Shared by the cross-attention kernels: parameters, valid-state masks, 4-D
+// tensor maps over [B, rows, heads, d] tensors and their TMA copies.
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include "bsa_internal.cuh"
+#include "tc_common.cuh"
+
+namespace bsa {
+namespace cross {
+
+constexpr int kTile = 128;           // query rows and keys of a tensor-core tile
+
+// Valid states of batch entry b.
+struct Keys {
+    const int32_t* kv_len;           // [B] or null
+    const uint8_t* key_mask;         // [B, M] or null
+    int M;
+    __device__ __forceinline__ int count(int b) const {
+        if (!kv_len) return M;
+        const int n = __ldg(kv_len + b);
+        return n < 0 ? 0 : (n > M ? M : n);
+    }
+    // Warp-collective: bit i of w[i / 32] = key base + i counts (128 keys); true if all 128 do.
+    __device__ __forceinline__ bool bits(int b, int len, int base, int lane, uint32_t* w) const {
+        if (!key_mask) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int n = len - base - 32 * i;
+                w[i] = n >= 32 ? 0xffffffffu : (n <= 0 ? 0u : (1u << n) - 1u);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int j = base + 32 * i + lane;
+                w[i] = __ballot_sync(0xffffffffu, j < len && __ldg(key_mask + (int64_t)b * M + j) != 0);
+            }
+        }
+        return (w[0] & w[1] & w[2] & w[3]) == 0xffffffffu;
+    }
+};
+
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int c, int row, int head, int b,
+                                            uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];"
+        ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(c), "r"(row), "r"(head), "r"(b), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void tma_store_4d(const CUtensorMap* map, uint32_t src, int c, int row, int head, int b) {
+    asm volatile("cp.async.bulk.tensor.4d.global.shared::cta.bulk_group [%0, {%2, %3, %4, %5}], [%1];"
+                 ::"l"(reinterpret_cast<uint64_t>(map)), "r"(src), "r"(c), "r"(row), "r"(head), "r"(b)
+                 : "memory");
+}
+__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+// The source of every committed store may be overwritten.
+__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+
+// bf16 [B, rows, heads, d] with element strides (batch, row, head) as a map of
+// [d, rows, heads, B], box [64, box_rows, 1, 1] with 128-byte swizzle.
+inline bool make_map_4d(CUtensorMap* m, const void* base, int64_t B, int64_t rows, int64_t heads, int d,
+                        const int64_t* st, int box_rows) {
+    auto enc = tc::get_encode();
+    if (!enc) return false;
+    cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)rows, (cuuint64_t)heads, (cuuint64_t)B};
+    cuuint64_t strides[3] = {(cuuint64_t)st[1] * 2, (cuuint64_t)st[2] * 2, (cuuint64_t)st[0] * 2};
+    cuuint32_t box[4] = {64u, (cuuint32_t)box_rows, 1u, 1u};
+    cuuint32_t estr[4] = {1u, 1u, 1u, 1u};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+inline void dense_strides(int64_t* st, int64_t rows, int64_t heads, int d) {
+    st[0] = rows * heads * d;
+    st[1] = heads * d;
+    st[2] = d;
+}
+
+}  // namespace cross
+
+// cross_fwd.cu: M > 0
+cudaError_t launch_cross_fwd_tc(const bsa_plan& p, const CrossArgs& a, void* o, float* lse, cudaStream_t s);
+
+}  // namespace bsa
