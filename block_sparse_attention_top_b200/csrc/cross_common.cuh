@@ -10,7 +10,8 @@
 namespace bsa {
 namespace cross {
 
-constexpr int kTile = 128;           // query rows and keys of a tensor-core tile
+constexpr int kTile = 128;           // query rows of a tensor-core tile
+constexpr int kKeys = 64;            // keys of one
 
 // Valid states of batch entry b.
 struct Keys {
@@ -22,24 +23,59 @@ struct Keys {
         const int n = __ldg(kv_len + b);
         return n < 0 ? 0 : (n > M ? M : n);
     }
-    // Warp-collective: bit i of w[i / 32] = key base + i counts (128 keys); true if all 128 do.
+    // Warp-collective: bit i of w[i / 32] = key base + i counts (kKeys of them); true if all do.
     __device__ __forceinline__ bool bits(int b, int len, int base, int lane, uint32_t* w) const {
         if (!key_mask) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int n = len - base - 32 * i;
-                w[i] = n >= 32 ? 0xffffffffu : (n <= 0 ? 0u : (1u << n) - 1u);
-            }
+            const int n = len - base;
+            w[0] = n >= 32 ? 0xffffffffu : (n <= 0 ? 0u : (1u << n) - 1u);
+            w[1] = n >= 64 ? 0xffffffffu : (n <= 32 ? 0u : (1u << (n - 32)) - 1u);
         } else {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < 2; ++i) {
                 const int j = base + 32 * i + lane;
                 w[i] = __ballot_sync(0xffffffffu, j < len && __ldg(key_mask + (int64_t)b * M + j) != 0);
             }
         }
-        return (w[0] & w[1] & w[2] & w[3]) == 0xffffffffu;
+        return (w[0] & w[1]) == 0xffffffffu;
     }
 };
+
+// One lane of a converged warp (the same one every time).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(p));
+    return p != 0;
+}
+
+// A bounded wait that lets the hardware suspend the thread between probes: for the roles that wait most of the
+// time (loads, output), whose spinning would take issue slots from the softmax warps.
+template <uint32_t kEvery>
+__device__ __noinline__ bool mbar_sleep(uint32_t bar, uint32_t parity, volatile tc::WaitCtl* ctl) {
+    const unsigned long long t0 = tc::globaltimer();
+    for (uint32_t n = 1;; ++n) {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 10000;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(bar), "r"(parity)
+            : "memory");
+        if (ok) return true;
+        if (kEvery == 0 || (n & 15) == 0) {
+            if (ctl->abort) return false;
+            if (tc::globaltimer() - t0 >= ctl->limit_ns) return false;
+        }
+    }
+}
+template <uint32_t kEvery>
+__device__ __forceinline__ bool warp_sleep(uint32_t bar, uint32_t parity, volatile tc::WaitCtl* ctl) {
+    return __all_sync(0xffffffffu, tc::mbar_test(bar, parity) || mbar_sleep<kEvery>(bar, parity, ctl));
+}
 
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int c, int row, int head, int b,
                                             uint32_t bar) {
@@ -47,6 +83,11 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
         "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];"
         ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(c), "r"(row), "r"(head), "r"(b), "r"(bar)
         : "memory");
+}
+__device__ __forceinline__ void prefetch_4d(const CUtensorMap* map, int c, int row, int head, int b) {
+    asm volatile("cp.async.bulk.prefetch.tensor.4d.L2.global [%0, {%1, %2, %3, %4}];"
+                 ::"l"(reinterpret_cast<uint64_t>(map)), "r"(c), "r"(row), "r"(head), "r"(b)
+                 : "memory");
 }
 __device__ __forceinline__ void tma_store_4d(const CUtensorMap* map, uint32_t src, int c, int row, int head, int b) {
     asm volatile("cp.async.bulk.tensor.4d.global.shared::cta.bulk_group [%0, {%2, %3, %4, %5}], [%1];"

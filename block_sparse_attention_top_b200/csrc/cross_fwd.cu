@@ -1,26 +1,27 @@
 // Cross attention forward on the tensor cores (formula in bsa.h).
 //
 // One CTA per SM walks items of two 128-row query tiles of one head; both
-// tiles use the same key tiles (128 keys), so K and V cross L2 once for 256
+// tiles use the same key tiles (64 keys), so K and V cross L2 once for 256
 // query rows.  Q, K and V come by TMA straight from the caller's strided
 // tensors, O leaves by TMA.
 //
 //   warps 0-3, 4-7  softmax of query tile 0, 1: a thread owns a row of S, its
-//                   running maximum and sum; it also stores the row of O
-//   warp 8          one thread issues every MMA:  ... PV0(t) QK0(t+1) PV1(t) QK1(t+1) ...
-//   warp 9          one thread loads Q tiles and the K ring
-//   warp 10         loads the V ring; in a tile with states that do not count
+//                   running maximum and sum
+//   warps 8-11      O / l to global memory, while the softmax warps are in the
+//                   next item
+//   warps 12, 13    MMAs of query tile 0, 1:  PV(t) QK(t+2)
+//   warp 14         one thread loads Q tiles and the K ring
+//   warp 15         loads the V ring; in a tile with states that do not count
 //                   it overwrites their rows with zeros (0 * NaN is NaN)
 //
-// TMEM: S0 [0,128) S1 [128,256) O0 [256,256+D) O1 [384,384+D).  P_g (bf16)
-// overwrites the first half of S_g: a thread has loaded its whole row of S
-// before it stores P, and QK_g(t+1) is issued behind PV_g(t), which reads P.
-// While one group exponentiates, the tensor cores work for the other.  When
-// S_g(t) is complete so is PV_g(t-1), which was issued before it, so a group
-// may rescale O_g without another barrier; it does so only when the maximum
-// grows by more than 2^8.  Walking on from item to item, the MMA thread issues
-// the next item's first QK_g behind this item's last PV_g, so the groups store
-// O while the next scores are made.
+// TMEM: two score buffers of 64 columns for each query tile, S0 [0,128)
+// S1 [128,256), and O0 [256,256+D) O1 [384,384+D).  P(t) in bf16 overwrites the
+// first half of S(t), columns its thread has read before.  The scores of tile
+// t+1 are made while the softmax warps work on tile t, so those never wait for
+// the tensor cores.  (With one buffer of 128 keys a group waited for PV and QK
+// between tiles: 4200 cycles for 128 keys of both query tiles.)
+// O_g is rescaled only when the maximum grows by more than 2^8; the softmax
+// warp then waits for PV(t-1).
 //
 // Waits are bounded as in attn_pp.cu.
 #include <algorithm>
@@ -33,21 +34,23 @@ namespace {
 using namespace tc;
 using namespace cross;
 
-constexpr int kMmaWarp = 8, kKWarp = 9, kVWarp = 10;
-constexpr int kThreads = 12 * 32;
+constexpr int kOutWarp = 8, kMmaWarp = 12, kKWarp = 14, kVWarp = 15;
+constexpr int kThreads = 16 * 32;
 constexpr uint32_t kTmemCols = 512, kColS = 0, kColO = 256;   // tile g at + g * 128
 
 template <int D>
 struct Smem {
-    static constexpr int kSlab = kTile * 128;                  // 128 rows x 64 columns
-    static constexpr int kTileBytes = kTile * D * 2;
-    static constexpr int kStages = D == 128 ? 2 : 4;           // of K and of V
+    static constexpr int kSlabQ = kTile * 128, kSlab = kKeys * 128;    // rows x 64 columns
+    static constexpr int kQBytes = kTile * D * 2, kTileBytes = kKeys * D * 2;
+    static constexpr int kStages = 4;                          // of K and of V
     static constexpr int offQ = 0;
-    static constexpr int offK = offQ + 2 * kTileBytes;
+    static constexpr int offK = offQ + 2 * kQBytes;
     static constexpr int offV = offK + kStages * kTileBytes;
-    static constexpr int offOut = offV + kStages * kTileBytes; // 8 warps x 32 rows x 64 columns
-    static constexpr int offBar = offOut + 8 * 4096;
-    static constexpr int offMisc = offBar + 32 * 8;
+    static constexpr int offOut = offV + kStages * kTileBytes; // 4 warps x 32 rows x 64 columns
+    static constexpr int kOutBytes = 4096;
+    static constexpr int offSum = offOut + 4 * kOutBytes;      // float l, m [2 items][2 tiles][128]
+    static constexpr int offBar = offSum + 2 * 2 * 2 * kTile * 4;
+    static constexpr int offMisc = offBar + 40 * 8;
     static constexpr int kAlloc = offMisc + 64 + 1024;         // room to align the base to 1024 B
 };
 
@@ -73,7 +76,7 @@ __device__ __forceinline__ bool item_at(const FwdP& p, int k, Item& it) {
     it.tile = (idx - bh * p.units) * p.per_item;
     it.ng = min(p.per_item, p.tiles - it.tile);
     it.len = p.keys.count(it.b);
-    it.nt = (it.len + kTile - 1) / kTile;
+    it.nt = (it.len + kKeys - 1) / kKeys;
     return true;
 }
 
@@ -94,17 +97,62 @@ struct Walk {
     }
 };
 
+// 2^x for a pair on the FMA pipe, x >= -126 after clamping: x = j + f with j = rint(x), a degree-4 polynomial for
+// 2^f on [-1/2, 1/2] (our own relative minimax fit, 2.6e-6), j added into the exponent field.
+__device__ __forceinline__ void ex2_fma2(float x0, float x1, float& y0, float& y1) {
+    x0 = fmaxf(x0, -126.f);
+    x1 = fmaxf(x1, -126.f);
+    float t0, t1, j0, j1, f0, f1, p0, p1;
+    fadd2(t0, t1, x0, x1, 12582912.f, 12582912.f);
+    fadd2(j0, j1, t0, t1, -12582912.f, -12582912.f);
+    ffma2(f0, f1, j0, j1, -1.f, -1.f, x0, x1);
+    ffma2(p0, p1, 0.0095701022f, 0.0095701022f, f0, f1, 0.0559178591f, 0.0559178591f);
+    ffma2(p0, p1, p0, p1, f0, f1, 0.2402474433f, 0.2402474433f);
+    ffma2(p0, p1, p0, p1, f0, f1, 0.6931217909f, 0.6931217909f);
+    ffma2(p0, p1, p0, p1, f0, f1, 0.9999992847f, 0.9999992847f);
+    y0 = __int_as_float(__float_as_int(p0) + (__float_as_int(t0) << 23));
+    y1 = __int_as_float(__float_as_int(p1) + (__float_as_int(t1) << 23));
+}
+constexpr int kFmaPairs = 2;         // pairs of every 8 that take the FMA pipe
+
+// 32 scores to 32 probabilities (16 bf16 pairs); adds them to acc.
+template <bool kMixed>
+__device__ __forceinline__ void exp_chunk(const uint32_t* x, float scale, float neg_m, float* acc, uint32_t* pk) {
+#pragma unroll
+    for (int c = 0; c < 32; c += 2) {
+        float x0, x1, p0, p1;
+        ffma2(x0, x1, __uint_as_float(x[c]), __uint_as_float(x[c + 1]), scale, scale, neg_m, neg_m);
+        if (kMixed && (c / 2) % 8 >= 8 - kFmaPairs) {
+            ex2_fma2(x0, x1, p0, p1);
+        } else {
+            p0 = ex2_mufu(x0);
+            p1 = ex2_mufu(x1);
+        }
+        const int u = (c / 2) & 1;
+        fadd2(acc[2 * u], acc[2 * u + 1], acc[2 * u], acc[2 * u + 1], p0, p1);
+        pk[c / 2] = pack_bf16(p0, p1);
+    }
+}
+
+// -inf where a state does not count
+__device__ __forceinline__ void mask_cols(uint32_t* s, uint32_t bits) {
+#pragma unroll
+    for (int c = 0; c < 32; ++c)
+        if (!(bits >> c & 1)) s[c] = __float_as_uint(-INFINITY);
+}
+
 template <int D, uint32_t kEvery>
 __global__ void __launch_bounds__(kThreads, 1)
 k_cross_fwd(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
             const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmO, const FwdP prm) {
     using L = Smem<D>;
     enum {
-        Q_FULL = 0, Q_EMPTY = 2, S_FULL = 4, P_FULL = 6, O_DONE = 8, V_RAW = 10, DRAIN = 11, K_FULL = 12,
+        Q_FULL = 0, Q_EMPTY = 2, S_FULL = 4, P_FULL = 8, PV_DONE = 12, O_DONE = 14, O_FREE = 16, DRAIN = 18, V_RAW = 20,
+        K_FULL = 21,
         K_EMPTY = K_FULL + L::kStages, V_FULL = K_EMPTY + L::kStages, V_EMPTY = V_FULL + L::kStages,
         kBars = V_EMPTY + L::kStages
     };
-    static_assert(kBars <= 32, "barrier slots");
+    static_assert(kBars <= 40, "barrier slots");
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char* smem = reinterpret_cast<unsigned char*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -112,12 +160,18 @@ k_cross_fwd(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUt
     auto bar = [&](int i) { return sbase + L::offBar + 8u * (uint32_t)i; };
     volatile WaitCtl* ctl = reinterpret_cast<volatile WaitCtl*>(smem + L::offMisc);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::offMisc + 16);
+    float* sums = reinterpret_cast<float*>(smem + L::offSum);
 
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     if (threadIdx.x == 0) {
         ctl->abort = 0;
         ctl->limit_ns = prm.wait_ns;
-        for (int i = 0; i < kBars; ++i) mbar_init(bar(i), i == P_FULL || i == P_FULL + 1 ? 128 : 1);
+        for (int i = 0; i < kBars; ++i) {
+            uint32_t count = 1;
+            if ((i >= P_FULL && i < P_FULL + 4) || (i >= O_FREE && i < O_FREE + 2)) count = 4;      // warps
+            if ((i >= K_EMPTY && i < V_FULL) || i >= V_EMPTY) count = 2;                            // MMA threads
+            mbar_init(bar(i), count);
+        }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == kMmaWarp) {
@@ -137,22 +191,31 @@ k_cross_fwd(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUt
             bool ok = true;
             Walk w;
             for (w.open(prm); w.ok && ok; w.next(prm), ++u) {
+                const int st = u % L::kStages;
+                if (u >= L::kStages && !(ok = mbar_sleep<kEvery>(bar(K_EMPTY + st), (u / L::kStages - 1) & 1, ctl))) break;
+                mbar_expect_tx(bar(K_FULL + st), L::kTileBytes);
+                for (int s = 0; s < D / 64; ++s)
+                    tma_load_4d(sbase + L::offK + st * L::kTileBytes + s * L::kSlab, &tmK, s * 64, w.t * kKeys,
+                                w.it.h / prm.G, w.it.b, bar(K_FULL + st));
                 if (w.t == 0)
                     for (int g = 0; g < w.it.ng && ok; ++g) {
-                        if (nq[g] > 0 && !(ok = mbar_wait<kEvery>(bar(Q_EMPTY + g), (nq[g] - 1) & 1, ctl))) break;
-                        mbar_expect_tx(bar(Q_FULL + g), L::kTileBytes);
+                        if (nq[g] > 0 && !(ok = mbar_sleep<kEvery>(bar(Q_EMPTY + g), (nq[g] - 1) & 1, ctl))) break;
+                        mbar_expect_tx(bar(Q_FULL + g), L::kQBytes);
                         for (int s = 0; s < D / 64; ++s)
-                            tma_load_4d(sbase + L::offQ + g * L::kTileBytes + s * L::kSlab, &tmQ, s * 64,
+                            tma_load_4d(sbase + L::offQ + g * L::kQBytes + s * L::kSlabQ, &tmQ, s * 64,
                                         (w.it.tile + g) * kTile, w.it.h, w.it.b, bar(Q_FULL + g));
                         ++nq[g];
                     }
-                if (!ok) break;
-                const int st = u % L::kStages;
-                if (u >= L::kStages && !(ok = mbar_wait<kEvery>(bar(K_EMPTY + st), (u / L::kStages - 1) & 1, ctl))) break;
-                mbar_expect_tx(bar(K_FULL + st), L::kTileBytes);
-                for (int s = 0; s < D / 64; ++s)
-                    tma_load_4d(sbase + L::offK + st * L::kTileBytes + s * L::kSlab, &tmK, s * 64, w.t * kTile,
-                                w.it.h / prm.G, w.it.b, bar(K_FULL + st));
+                if (!ok) { ++u; break; }
+                // The next item's Q, on its way to L2 while this item runs: a slab behind every K tile but the first
+                // few, since a later load waits for the copies issued before it.
+                if (w.t >= 2 && w.t < 2 + 2 * (D / 64)) {
+                    Walk n = w;
+                    ++n.k;
+                    n.seek(prm);
+                    const int g = (w.t - 2) / (D / 64), s = (w.t - 2) % (D / 64);
+                    if (n.ok && g < n.it.ng) prefetch_4d(&tmQ, s * 64, (n.it.tile + g) * kTile, n.it.h, n.it.b);
+                }
             }
             if (!ok) { ctl->abort = 1; record_error(prm.err, BSA_EDEVICE, -1); }
             // every tile this thread issued lands before the CTA exits
@@ -168,9 +231,9 @@ k_cross_fwd(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUt
         Walk w;
         for (w.open(prm); w.ok; w.next(prm), ++u) {
             const int st = u % L::kStages;
-            if (u >= L::kStages && !(ok = warp_wait<kEvery>(bar(V_EMPTY + st), (u / L::kStages - 1) & 1, ctl))) break;
-            uint32_t bits[4];
-            const bool all = prm.keys.bits(w.it.b, w.it.len, w.t * kTile, lane, bits);
+            if (u >= L::kStages && !(ok = warp_sleep<kEvery>(bar(V_EMPTY + st), (u / L::kStages - 1) & 1, ctl))) break;
+            uint32_t bits[2];
+            const bool all = prm.keys.bits(w.it.b, w.it.len, w.t * kKeys, lane, bits);
             // rows past M are zero already: the copy fills them
             const bool fix = !all && (prm.keys.key_mask || w.it.len < prm.keys.M);
             const uint32_t full = bar(fix ? V_RAW : V_FULL + st);
@@ -178,7 +241,7 @@ k_cross_fwd(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUt
             if (lane == 0) {
                 mbar_expect_tx(full, L::kTileBytes);
                 for (int s = 0; s < D / 64; ++s)
-                    tma_load_4d(dst + s * L::kSlab, &tmV, s * 64, w.t * kTile, w.it.h / prm.G, w.it.b, full);
+                    tma_load_4d(dst + s * L::kSlab, &tmV, s * 64, w.t * kKeys, w.it.h / prm.G, w.it.b, full);
             }
             if (fix) {
                 const bool landed = warp_wait<kEvery>(full, raw & 1, ctl);
@@ -188,7 +251,7 @@ k_cross_fwd(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUt
                     break;
                 }
                 ++raw;
-                for (int i = 0; i < kTile; ++i)                  // a row of a slab: 8 lanes of 16 bytes
+                for (int i = 0; i < kKeys; ++i)                  // a row of a slab: 8 lanes of 16 bytes
                     if (!(bits[i / 32] >> (i % 32) & 1) && lane < D / 8)
                         *reinterpret_cast<uint4*>(smem + (dst - sbase) + (lane / 8) * L::kSlab + i * 128 +
                                                   (lane % 8) * 16) = make_uint4(0, 0, 0, 0);
@@ -200,179 +263,221 @@ k_cross_fwd(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUt
         if (!ok && lane == 0) { ctl->abort = 1; record_error(prm.err, BSA_EDEVICE, -2); }
         for (uint32_t st = 0; st < L::kStages; ++st)
             if (u > st) mbar_drain(bar(V_FULL + st), ((u - 1 - st) / L::kStages) & 1);
-    } else if (warp == kMmaWarp) {
-        // --------------------------------------------------------------- MMA issuer
-        if (lane == 0) {
-            constexpr uint32_t idesc_qk = instr_desc(kTile, 0), idesc_pv = instr_desc(D, 1);
-            uint32_t uk = 0, uv = 0, nq[2] = {0, 0}, np[2] = {0, 0};
-            bool ok = true;
-            // S_g = Q_g K^T of step w, whose K tile is number uk
-            auto qk = [&](const Walk& w, int g) {
-                if (w.t == 0) {
-                    if (!mbar_wait<kEvery>(bar(Q_FULL + g), nq[g] & 1, ctl)) return false;
-                    ++nq[g];
-                }
-                const int st = uk % L::kStages;
-                if (!mbar_wait<kEvery>(bar(K_FULL + st), (uk / L::kStages) & 1, ctl)) return false;
-                fence_after();
+    } else if (warp == kMmaWarp || warp == kMmaWarp + 1) {
+        // -------------------------------------------------------------- MMA issuers
+        // The whole warp walks and waits, so that descriptors stay in uniform registers; one lane issues.
+        constexpr uint32_t idesc_qk = instr_desc(kKeys, 0), idesc_pv = instr_desc(D, 1);
+        const int g = __shfl_sync(0xffffffffu, warp, 0) - kMmaWarp;
+        const uint32_t ts = tmem + kColS + g * 128, to = tmem + kColO + g * 128;
+        const uint32_t q_tile = sbase + L::offQ + g * L::kQBytes;
+        uint32_t uk = 0, uv = 0, sk = 0, sp = 0, nq = 0, no = 0;   // ring tiles; this group's S, P, Q, O
+        bool ok = true;
+        // K tile uk of step w, and Q_g with an item's first, have landed
+        auto qk_ready = [&](const Walk& w) {
+            return warp_wait<kEvery>(bar(K_FULL + uk % L::kStages), (uk / L::kStages) & 1, ctl) &&
+                   (w.t > 0 || g >= w.it.ng || warp_wait<kEvery>(bar(Q_FULL + g), nq++ & 1, ctl));
+        };
+        // S[sk & 1] = Q_g K^T; a step without this query tile only passes the stage on (one lane)
+        auto qk = [&](const Walk& w) {
+            const int st = uk % L::kStages;
+            if (g < w.it.ng) {
 #pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk) {
-                    const uint32_t off = (kk / 4) * L::kSlab + (kk % 4) * 32;
-                    mma_ss(tmem + kColS + g * 128, smem_desc(sbase + L::offQ + g * L::kTileBytes + off, 16, 1024),
-                           smem_desc(sbase + L::offK + st * L::kTileBytes + off, 16, 1024), idesc_qk, kk > 0);
-                }
-                commit(bar(S_FULL + g));
+                for (int kk = 0; kk < D / 16; ++kk)
+                    mma_ss(ts + (sk & 1) * kKeys, smem_desc(q_tile + (kk / 4) * L::kSlabQ + (kk % 4) * 32, 16, 1024),
+                           smem_desc(sbase + L::offK + st * L::kTileBytes + (kk / 4) * L::kSlab + (kk % 4) * 32, 16, 1024),
+                           idesc_qk, kk > 0);
+                commit(bar(S_FULL + 2 * g + (sk & 1)));
+                commit(bar(K_EMPTY + st));
                 if (w.t == w.it.nt - 1) commit(bar(Q_EMPTY + g));
-                return true;
-            };
-            Walk cur, nxt;
-            cur.open(prm);
-            if (cur.ok) {
-                for (int g = 0; g < cur.it.ng && ok; ++g) ok = qk(cur, g);
-                if (ok) commit(bar(K_EMPTY + uk % L::kStages));
-                ++uk;
+            } else {
+                mbar_arrive(bar(K_EMPTY + st));
             }
-            while (cur.ok && ok) {
-                nxt = cur;
-                nxt.next(prm);
-                const int st = uv % L::kStages;
-                for (int g = 0; g < 2 && ok; ++g) {
-                    if (g < cur.it.ng) {
-                        if (!(ok = mbar_wait<kEvery>(bar(P_FULL + g), np[g] & 1, ctl))) break;
-                        ++np[g];
-                        if (!(ok = mbar_wait<kEvery>(bar(V_FULL + st), (uv / L::kStages) & 1, ctl))) break;
-                        fence_after();
-#pragma unroll
-                        for (int kk = 0; kk < kTile / 16; ++kk)
-                            mma_ts(tmem + kColO + g * 128, tmem + kColS + g * 128 + kk * 8,
-                                   smem_desc(sbase + L::offV + st * L::kTileBytes + kk * 16 * 128, L::kSlab, 1024),
-                                   idesc_pv, cur.t > 0 || kk > 0);
-                        if (cur.t == cur.it.nt - 1) commit(bar(O_DONE + g));
-                    }
-                    if (nxt.ok && g < nxt.it.ng) ok = qk(nxt, g);
-                }
-                if (!ok) break;
-                commit(bar(V_EMPTY + st));
-                ++uv;
-                if (nxt.ok) {
-                    commit(bar(K_EMPTY + uk % L::kStages));
-                    ++uk;
-                }
-                cur = nxt;
-            }
-            if (!ok) { ctl->abort = 1; record_error(prm.err, BSA_EDEVICE, -3); }
-            commit(bar(DRAIN));                          // everything issued completes before TMEM is freed
-            mbar_drain(bar(DRAIN), 0);
+        };
+        Walk cur, ahead;                                 // ahead: the step whose scores are made next
+        cur.open(prm);
+        ahead = cur;
+        for (int i = 0; i < 2 && ahead.ok && (ok = qk_ready(ahead)); ++i) {
+            fence_after();
+            if (elect_one()) qk(ahead);
+            __syncwarp();
+            ++uk;
+            sk += g < ahead.it.ng;
+            ahead.next(prm);
         }
-    } else if (warp < kMmaWarp) {
+        for (; cur.ok && ok; cur.next(prm), ++uv) {
+            const int st = uv % L::kStages;
+            // everything but P first: a warp that polls behind its own MMAs waits until the tensor cores have taken them
+            if (!(ok = warp_wait<kEvery>(bar(V_FULL + st), (uv / L::kStages) & 1, ctl))) break;
+            if (ahead.ok && !(ok = qk_ready(ahead))) break;
+            if (g < cur.it.ng) {
+                // the item before this one has been read out of O_g
+                if (cur.t == 0 && no++ > 0 && !(ok = warp_wait<kEvery>(bar(O_FREE + g), no & 1, ctl))) break;
+                if (!(ok = warp_wait<kEvery>(bar(P_FULL + 2 * g + (sp & 1)), (sp >> 1) & 1, ctl))) break;
+            }
+            fence_after();
+            if (elect_one()) {
+                if (g < cur.it.ng) {
+#pragma unroll
+                    for (int kk = 0; kk < kKeys / 16; ++kk)
+                        mma_ts(to, ts + (sp & 1) * kKeys + kk * 8,
+                               smem_desc(sbase + L::offV + st * L::kTileBytes + kk * 16 * 128, L::kSlab, 1024), idesc_pv,
+                               cur.t > 0 || kk > 0);
+                    commit(bar(PV_DONE + g));
+                    commit(bar(V_EMPTY + st));
+                    if (cur.t == cur.it.nt - 1) commit(bar(O_DONE + g));
+                } else {
+                    mbar_arrive(bar(V_EMPTY + st));
+                }
+                if (ahead.ok) qk(ahead);
+            }
+            __syncwarp();
+            sp += g < cur.it.ng;
+            if (ahead.ok) {
+                ++uk;
+                sk += g < ahead.it.ng;
+                ahead.next(prm);
+            }
+        }
+        if (!ok && lane == 0) { ctl->abort = 1; record_error(prm.err, BSA_EDEVICE, -3); }
+        if (elect_one()) {
+            commit(bar(DRAIN + g));                      // everything issued completes before TMEM is freed
+            mbar_drain(bar(DRAIN + g), 0);
+        }
+        __syncwarp();
+    } else if (warp < kOutWarp) {
         // ------------------------------------------------------------------ softmax
         const int g = warp / 4, quad = warp & 3;
         const uint32_t lane_base = (uint32_t)(32 * quad) << 16;
         const uint32_t ts = tmem + lane_base + kColS + g * 128, to = tmem + lane_base + kColO + g * 128;
-        unsigned char* stage = smem + L::offOut + warp * 4096;
-        const uint32_t stage_u32 = sbase + L::offOut + warp * 4096;
-        uint32_t ns = 0, no = 0;
+        uint32_t ns = 0, done = 0;
         bool ok = true;
         Item it;
         for (int k = 0; ok && item_at(prm, k, it); ++k) {
-            if (g >= it.ng) continue;
-            const int row0 = (it.tile + g) * kTile + 32 * quad;       // first query row of this warp
+            if (g >= it.ng || it.nt == 0) continue;
             float m = -INFINITY, l = 0.f;
             for (int t = 0; t < it.nt; ++t, ++ns) {
-                uint32_t bits[4];
-                const bool all = prm.keys.bits(it.b, it.len, t * kTile, lane, bits);
-                if (!(ok = warp_wait<kEvery>(bar(S_FULL + g), ns & 1, ctl))) break;
+                const uint32_t tsb = ts + (ns & 1) * kKeys;
+                uint32_t bits[2];
+                const bool all = prm.keys.bits(it.b, it.len, t * kKeys, lane, bits);
+                if (!(ok = warp_wait<kEvery>(bar(S_FULL + 2 * g + (ns & 1)), (ns >> 1) & 1, ctl))) break;
                 fence_after();
-                uint32_t sv[kTile];
-#pragma unroll
-                for (int c = 0; c < kTile / 32; ++c) tmem_ld32(ts + c * 32, sv + 32 * c);
+                uint32_t sv[kKeys];
+                tmem_ld32(tsb, sv);
+                tmem_ld32(tsb + 32, sv + 32);
                 tmem_wait_ld();
                 if (!all) {
-#pragma unroll
-                    for (int c = 0; c < kTile; ++c)
-                        if (!(bits[c / 32] >> (c % 32) & 1)) sv[c] = __float_as_uint(-INFINITY);
+                    mask_cols(sv, bits[0]);
+                    mask_cols(sv + 32, bits[1]);
                 }
-                const float mx = row_max<kTile>(sv, -INFINITY) * prm.scale_log2;
+                const float mx = row_max<kKeys>(sv, -INFINITY) * prm.scale_log2;
                 // lazy maximum: P stays below 2^8
                 const bool grow = t > 0 && mx > m + 8.f;
                 const float alpha = grow ? ex2_mufu(m - mx) : 1.f;
                 if (t == 0 || grow) m = mx;
                 const float neg_m = m == -INFINITY ? 0.f : -m;        // no valid state so far
-                float acc[8] = {};
-                uint32_t pk[kTile / 2];
-#pragma unroll
-                for (int c = 0; c < kTile; c += 2) {
-                    float x0, x1;
-                    ffma2(x0, x1, __uint_as_float(sv[c]), __uint_as_float(sv[c + 1]), prm.scale_log2, prm.scale_log2,
-                          neg_m, neg_m);
-                    const float p0 = ex2_mufu(x0), p1 = ex2_mufu(x1);
-                    const int u = (c / 2) & 3;
-                    fadd2(acc[2 * u], acc[2 * u + 1], acc[2 * u], acc[2 * u + 1], p0, p1);
-                    pk[c / 2] = pack_bf16(p0, p1);
+                float acc[4] = {};
+                uint32_t pk[kKeys / 2];
+                if (all) {
+                    exp_chunk<true>(sv, prm.scale_log2, neg_m, acc, pk);
+                    tmem_st16(tsb, pk);
+                    exp_chunk<true>(sv + 32, prm.scale_log2, neg_m, acc, pk + 16);
+                    tmem_st16(tsb + 16, pk + 16);
+                } else {
+                    exp_chunk<false>(sv, prm.scale_log2, neg_m, acc, pk);
+                    tmem_st16(tsb, pk);
+                    exp_chunk<false>(sv + 32, prm.scale_log2, neg_m, acc, pk + 16);
+                    tmem_st16(tsb + 16, pk + 16);
                 }
+                l = l * alpha + ((acc[0] + acc[1]) + (acc[2] + acc[3]));
                 if (__any_sync(0xffffffffu, grow)) {
-#pragma unroll
-                    for (int c = 0; c < D / 32; ++c) {
-                        uint32_t o[32];
-                        tmem_ld32(to + c * 32, o);
+                    // PV(t-1) is the tile before this one; PV(t-2) was complete before S(t) was, so the parity is exact
+                    if (!(ok = warp_wait<kEvery>(bar(PV_DONE + g), (ns - 1) & 1, ctl))) break;
+                    fence_after();
+#pragma unroll 1
+                    for (int c = 0; c < D; c += 32) {
+                        tmem_ld32(to + c, sv);
                         tmem_wait_ld();
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-                        tmem_st32(to + c * 32, o);
+                        for (int e = 0; e < 32; ++e) sv[e] = __float_as_uint(__uint_as_float(sv[e]) * alpha);
+                        tmem_st32(to + c, sv);
                     }
                 }
-#pragma unroll
-                for (int c = 0; c < kTile / 64; ++c) tmem_st32(ts + c * 32, pk + 32 * c);
-                l = l * alpha + (((acc[0] + acc[1]) + (acc[2] + acc[3])) + ((acc[4] + acc[5]) + (acc[6] + acc[7])));
+                if (t == it.nt - 1) {                                 // for the output warps
+                    float* slot = sums + ((done & 1) * 2 + g) * 2 * kTile + 32 * quad + lane;
+                    slot[0] = l;
+                    slot[kTile] = m;
+                    ++done;
+                }
                 tmem_wait_st();
                 fence_before();
-                mbar_arrive(bar(P_FULL + g));
-            }
-            if (!ok) break;
-            // epilogue: O / l (zeros for a row without a valid state) through shared memory
-            if (it.nt > 0) {
-                if (!(ok = warp_wait<kEvery>(bar(O_DONE + g), no & 1, ctl))) break;
-                ++no;
-                fence_after();
-            }
-            const float inv = l == 0.f ? 0.f : 1.f / l;
-            const int n = row0 + lane;
-            if (prm.lse && n < prm.N)
-                prm.lse[((int64_t)it.b * prm.H + it.h) * prm.N + n] =
-                    l == 0.f ? -INFINITY : 0.69314718055994531f * (m + log2f(l));
-#pragma unroll
-            for (int s = 0; s < D / 64; ++s) {
-                uint32_t o[64];
-                if (it.nt > 0) {
-                    tmem_ld32(to + s * 64, o);
-                    tmem_ld32(to + s * 64 + 32, o + 32);
-                    tmem_wait_ld();
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 64; ++e) o[e] = 0u;
-                }
-                if (lane == 0) bulk_wait_read();                      // the slab before this one has left
                 __syncwarp();
-#pragma unroll
-                for (int c = 0; c < 8; ++c) {
-                    uint4 v;
-                    v.x = pack_bf16(__uint_as_float(o[8 * c + 0]) * inv, __uint_as_float(o[8 * c + 1]) * inv);
-                    v.y = pack_bf16(__uint_as_float(o[8 * c + 2]) * inv, __uint_as_float(o[8 * c + 3]) * inv);
-                    v.z = pack_bf16(__uint_as_float(o[8 * c + 4]) * inv, __uint_as_float(o[8 * c + 5]) * inv);
-                    v.w = pack_bf16(__uint_as_float(o[8 * c + 6]) * inv, __uint_as_float(o[8 * c + 7]) * inv);
-                    *reinterpret_cast<uint4*>(stage + lane * 128 + ((c ^ (lane & 7)) * 16)) = v;
-                }
-                fence_proxy_async();
-                __syncwarp();
-                if (lane == 0 && row0 < prm.N) {
-                    tma_store_4d(&tmO, stage_u32, s * 64, row0, it.h, it.b);
-                    bulk_commit();
-                }
+                if (lane == 0) mbar_arrive(bar(P_FULL + 2 * g + (ns & 1)));
             }
-            fence_before();                                           // O was read: ordered before P of the next item
         }
         if (!ok) { ctl->abort = 1; record_error(prm.err, BSA_EDEVICE, -4); }
         tmem_wait_st();
+        tmem_wait_ld();
+    } else if (warp < kMmaWarp) {
+        // ------------------------------------------------------------------- output
+        const int quad = warp & 3;
+        const uint32_t to = tmem + ((uint32_t)(32 * quad) << 16) + kColO;
+        unsigned char* stage = smem + L::offOut + quad * L::kOutBytes;
+        uint32_t done[2] = {0, 0};
+        bool ok = true;
+        Item it;
+        for (int k = 0; ok && item_at(prm, k, it); ++k)
+            for (int g = 0; g < it.ng; ++g) {
+                const int row0 = (it.tile + g) * kTile + 32 * quad, n = row0 + lane;
+                float l = 0.f, m = 0.f;
+                if (it.nt > 0) {
+                    // the last PV is complete, so its P and with it l and m were written before
+                    if (!(ok = warp_sleep<kEvery>(bar(O_DONE + g), done[g] & 1, ctl))) break;
+                    fence_after();
+                    const float* slot = sums + ((done[g] & 1) * 2 + g) * 2 * kTile + 32 * quad + lane;
+                    l = slot[0];
+                    m = slot[kTile];
+                    ++done[g];
+                }
+                const float inv = l == 0.f ? 0.f : 1.f / l;           // zeros for a row without a valid state
+                if (prm.lse && n < prm.N)
+                    prm.lse[((int64_t)it.b * prm.H + it.h) * prm.N + n] =
+                        l == 0.f ? -INFINITY : 0.69314718055994531f * (m + log2f(l));
+#pragma unroll
+                for (int s = 0; s < D / 64; ++s) {
+                    uint32_t o[64];
+                    if (it.nt > 0) {
+                        tmem_ld32(to + g * 128 + s * 64, o);
+                        tmem_ld32(to + g * 128 + s * 64 + 32, o + 32);
+                        tmem_wait_ld();
+                        if (s == D / 64 - 1) {                        // O_g may take the next item
+                            fence_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(bar(O_FREE + g));
+                        }
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 64; ++e) o[e] = 0u;
+                    }
+                    if (lane == 0) bulk_wait_read();                  // the slab before this one has left
+                    __syncwarp();
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) {
+                        uint4 v;
+                        v.x = pack_bf16(__uint_as_float(o[8 * c + 0]) * inv, __uint_as_float(o[8 * c + 1]) * inv);
+                        v.y = pack_bf16(__uint_as_float(o[8 * c + 2]) * inv, __uint_as_float(o[8 * c + 3]) * inv);
+                        v.z = pack_bf16(__uint_as_float(o[8 * c + 4]) * inv, __uint_as_float(o[8 * c + 5]) * inv);
+                        v.w = pack_bf16(__uint_as_float(o[8 * c + 6]) * inv, __uint_as_float(o[8 * c + 7]) * inv);
+                        *reinterpret_cast<uint4*>(stage + lane * 128 + ((c ^ (lane & 7)) * 16)) = v;
+                    }
+                    fence_proxy_async();
+                    __syncwarp();
+                    if (lane == 0 && row0 < prm.N) {
+                        tma_store_4d(&tmO, smem_u32(stage), s * 64, row0, it.h, it.b);
+                        bulk_commit();
+                    }
+                }
+            }
+        if (!ok) { ctl->abort = 1; record_error(prm.err, BSA_EDEVICE, -5); }
         tmem_wait_ld();
         if (lane == 0) bulk_wait();
     }
@@ -391,8 +496,8 @@ cudaError_t launch_t(const bsa_plan& p, const CrossArgs& a, const FwdP& prm, voi
     CUtensorMap mq, mk, mv, mo;
     int64_t so[3];
     dense_strides(so, p.N, p.H, D);
-    if (!make_map_4d(&mq, a.q, p.B, p.N, p.H, D, a.st, kTile) || !make_map_4d(&mk, a.k, p.B, a.M, a.Hkv, D, a.st + 3, kTile) ||
-        !make_map_4d(&mv, a.v, p.B, a.M, a.Hkv, D, a.st + 6, kTile) || !make_map_4d(&mo, o, p.B, p.N, p.H, D, so, 32))
+    if (!make_map_4d(&mq, a.q, p.B, p.N, p.H, D, a.st, kTile) || !make_map_4d(&mk, a.k, p.B, a.M, a.Hkv, D, a.st + 3, kKeys) ||
+        !make_map_4d(&mv, a.v, p.B, a.M, a.Hkv, D, a.st + 6, kKeys) || !make_map_4d(&mo, o, p.B, p.N, p.H, D, so, 32))
         return cudaErrorInvalidValue;
     cudaError_t e = cudaFuncSetAttribute(k_cross_fwd<D, kEvery>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc);
     if (e != cudaSuccess) return e;
