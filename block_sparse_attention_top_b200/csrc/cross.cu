@@ -160,8 +160,7 @@ unsigned row_grid(int64_t rows) { return (unsigned)((rows + kRowWarps - 1) / kRo
 }  // namespace
 
 size_t cross_ws_bytes(const bsa_plan& p, int64_t M, int Hkv, bool backward) {
-    (void)M; (void)Hkv;
-    return backward ? align_up((size_t)p.B * p.H * p.N * sizeof(float)) : 0;
+    return backward ? cross_bwd_ws_bytes(p, M, Hkv) : 0;
 }
 
 cudaError_t launch_cross(const bsa_plan& p, const CrossArgs& a, void* o, float* lse, void*, cudaStream_t s) {
@@ -174,6 +173,7 @@ cudaError_t launch_cross(const bsa_plan& p, const CrossArgs& a, void* o, float* 
 
 cudaError_t launch_cross_bwd(const bsa_plan& p, const CrossArgs& a, const void* o, const float* lse, const void* d_o,
                              void* dq, void* dk, void* dv, void* ws, cudaStream_t s) {
+    if (a.M > 0) return launch_cross_bwd_tc(p, a, o, lse, d_o, dq, dk, dv, ws, s);
     const CrossP c = cross_params(p, a);
     const __nv_bfloat16* g = (const __nv_bfloat16*)d_o;
     auto kq = p.d == 128 ? k_cross_dq<128> : k_cross_dq<64>;

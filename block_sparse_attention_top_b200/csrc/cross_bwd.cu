@@ -1,0 +1,919 @@
+// Gradient of the cross attention on the tensor cores (formulas in bsa.h).
+//
+// Two passes, each of which keeps its sums in TMEM and needs no atomics, so
+// the same inputs give the same bits:
+//   k_cross_dq   a CTA owns a query tile and walks the keys:
+//                S = Q K^T, dP = dO V^T, dS = P * (dP - D), dQ += dS K;
+//   k_cross_dkv  a CTA owns a key tile and walks a share of the query tokens:
+//                S^T = K Q^T, dP^T = V dO^T, dV += P^T dO, dK += dS^T Q.
+// Making S and dP twice costs two more products than one pass would, 7 for 5,
+// but one pass would have to add dQ tiles (fp32, once for every key tile) in
+// memory: more traffic than the two products take time, and an order that
+// depends on scheduling.  A third kernel adds the key side's shares in order.
+//
+// Both passes work in tiles of 64 on the side they walk, with two buffers of
+// S and dP in TMEM; softmax group 0 (warps 0-3) takes the even tiles and
+// group 1 (warps 4-7) the odd ones, a thread per row of the owned side.  P and
+// dS (bf16) overwrite the S and dP that their thread has read.  The tensor
+// cores make S and dP of tile u+2 behind the products that read tile u.
+//
+// Waits are bounded as in attn_pp.cu.
+#include <algorithm>
+
+#include "cross_common.cuh"
+
+namespace bsa {
+namespace {
+
+using namespace tc;
+using namespace cross;
+
+constexpr int kRowWarp = 8, kMmaWarp = 12;
+constexpr int kThreads = 16 * 32;
+constexpr uint32_t kTmemCols = 512;
+constexpr float kLog2e = 1.4426950408889634f;
+
+__device__ __forceinline__ void fmul2(float& d0, float& d1, float a0, float a1, float b0, float b1) {
+    asm("{\n\t.reg .b64 ra, rb, rd;\n\t"
+        "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
+        "mul.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+        : "=f"(d0), "=f"(d1)
+        : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
+}
+// Address of 16-byte chunk c of row r in a tile of 64-column slabs with 128-byte swizzle.
+__device__ __forceinline__ uint32_t swizzled(int r, int c, int slab_bytes) {
+    return (uint32_t)((c / 8) * slab_bytes + r * 128 + (((c % 8) ^ (r & 7)) * 16));
+}
+__device__ __forceinline__ float dot8(uint4 a, uint4 b) {
+    const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        s += __uint_as_float(x[i] << 16) * __uint_as_float(y[i] << 16) +
+             __uint_as_float(x[i] & 0xffff0000u) * __uint_as_float(y[i] & 0xffff0000u);
+    return s;
+}
+
+// Shared prologue: barriers, TMEM.  Shared epilogue: TMEM.
+template <int kBars, typename Count>
+__device__ __forceinline__ uint32_t begin_cta(uint32_t bar0, volatile WaitCtl* ctl, uint32_t* tmem_slot,
+                                              unsigned long long wait_ns, Count count) {
+    if (threadIdx.x == 0) {
+        ctl->abort = 0;
+        ctl->limit_ns = wait_ns;
+        for (int i = 0; i < kBars; ++i) mbar_init(bar0 + 8 * i, count(i));
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (threadIdx.x / 32 == kMmaWarp) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
+                     ::"r"(smem_u32(tmem_slot)), "r"(kTmemCols) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    fence_before();
+    __syncthreads();
+    fence_after();
+    return *tmem_slot;
+}
+__device__ __forceinline__ void end_cta(uint32_t tmem) {
+    fence_before();
+    __syncthreads();
+    fence_after();
+    if (threadIdx.x / 32 == kMmaWarp)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
+}
+
+// ------------------------------------------------------------------ query side
+// warps 0-7 softmax, 8-11 rows (D, then dQ to memory), 12 MMA, 13 K ring,
+// 14 V ring, 15 Q and dO.  Q and dO go to TMEM (tcgen05.cp), so that S and dP
+// read only K and V from shared memory.
+struct DqP {
+    Keys keys;
+    const __nv_bfloat16* o;
+    const float* lse;
+    float* dsum;
+    int32_t* err;
+    int N, H, G, tiles, items;
+    float scale, scale_log2;
+    unsigned long long wait_ns;
+};
+
+template <int D>
+struct DqSmem {
+    static constexpr int kSlabQ = kTile * 128, kSlab = kKeys * 128;
+    static constexpr int kQBytes = kTile * D * 2, kTileBytes = kKeys * D * 2;
+    static constexpr int kStages = 4;
+    static constexpr int offQ = 0;                                 // Q, dO
+    static constexpr int offK = offQ + 2 * kQBytes;
+    static constexpr int offV = offK + kStages * kTileBytes;
+    static constexpr int offOut = offV + kStages * kTileBytes;     // 4 warps x 32 rows x 64 columns
+    static constexpr int offRows = offOut + 4 * 4096;              // float lse, D [2 items][128]
+    static constexpr int offBar = offRows + 2 * 2 * kTile * 4;
+    static constexpr int offMisc = offBar + 48 * 8;
+    static constexpr int kAlloc = offMisc + 64 + 1024;
+    static constexpr uint32_t colS = 0, colDP = 128, colQ = 256, colDO = 256 + D / 2, colDQ = 384;
+};
+
+struct DqItem {
+    int b, h, tile, len, nt;
+};
+__device__ __forceinline__ bool item_at(const DqP& p, int k, DqItem& it) {
+    const int idx = k * gridDim.x + blockIdx.x;
+    if (idx >= p.items) return false;
+    const int bh = idx / p.tiles;
+    it.b = bh / p.H;
+    it.h = bh % p.H;
+    it.tile = idx - bh * p.tiles;
+    it.len = p.keys.count(it.b);
+    it.nt = (it.len + kKeys - 1) / kKeys;
+    return true;
+}
+struct DqWalk {
+    DqItem it;
+    int k = 0, t = 0;
+    bool ok;
+    __device__ __forceinline__ void seek(const DqP& p) {
+        while ((ok = item_at(p, k, it)) && it.nt == 0) ++k;
+    }
+    __device__ __forceinline__ void next(const DqP& p) {
+        if (++t < it.nt) return;
+        next_item(p);
+    }
+    __device__ __forceinline__ void next_item(const DqP& p) {
+        t = 0;
+        ++k;
+        seek(p);
+    }
+    __device__ __forceinline__ bool last() const { return t == it.nt - 1; }
+};
+
+template <int D, uint32_t kEvery>
+__global__ void __launch_bounds__(kThreads, 1)
+k_cross_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+           const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmDO,
+           const __grid_constant__ CUtensorMap tmDQ, const DqP prm) {
+    using L = DqSmem<D>;
+    enum {
+        QD_FULL = 0, QD_EMPTY, AB_FREE, S_FULL, DS_FULL = S_FULL + 2, ROWS_FULL = DS_FULL + 2, ROWS_EMPTY = ROWS_FULL + 2,
+        DQ_DONE = ROWS_EMPTY + 2, DQ_FREE, DRAIN, K_RAW, K_FULL, K_EMPTY = K_FULL + L::kStages,
+        V_FULL = K_EMPTY + L::kStages, V_EMPTY = V_FULL + L::kStages, kBars = V_EMPTY + L::kStages
+    };
+    static_assert(kBars <= 48, "barrier slots");
+    extern __shared__ __align__(1024) unsigned char smem_raw[];
+    unsigned char* smem = reinterpret_cast<unsigned char*>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t sbase = smem_u32(smem);
+    auto bar = [&](int i) { return sbase + L::offBar + 8u * (uint32_t)i; };
+    volatile WaitCtl* ctl = reinterpret_cast<volatile WaitCtl*>(smem + L::offMisc);
+    float* row_vals = reinterpret_cast<float*>(smem + L::offRows);
+    const uint32_t tmem = begin_cta<kBars>(bar(0), ctl, reinterpret_cast<uint32_t*>(smem + L::offMisc + 16), prm.wait_ns,
+                                           [](int i) -> uint32_t {
+                                               if (i == QD_EMPTY) return 5;                       // copies, 4 row warps
+                                               if (i == ROWS_EMPTY || i == ROWS_EMPTY + 1) return 8;
+                                               if ((i >= DS_FULL && i < ROWS_EMPTY) || i == DQ_FREE) return 4;
+                                               return 1;
+                                           });
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
+    bool ok = true;
+
+    if (warp == kMmaWarp) {
+        constexpr uint32_t idesc_s = instr_desc(kKeys, 0), idesc_dq = instr_desc(D, 1);
+        uint32_t ua = 0, uc = 0, items_a = 0, items_c = 0;        // steps and items: scores made, dQ added
+        DqWalk cur, ahead;
+        cur.seek(prm);
+        ahead = cur;
+        // everything the scores of `ahead` read is there
+        auto ready = [&] {
+            const uint32_t st = ua % L::kStages, ph = (ua / L::kStages) & 1;
+            if (!warp_wait<kEvery>(bar(K_FULL + st), ph, ctl) || !warp_wait<kEvery>(bar(V_FULL + st), ph, ctl)) return false;
+            if (ahead.t > 0) return true;
+            // the item's Q and dO to TMEM, once the item before it has made its last scores
+            if (items_a > 0 && !warp_wait<kEvery>(bar(AB_FREE), (items_a - 1) & 1, ctl)) return false;
+            if (!warp_wait<kEvery>(bar(QD_FULL), items_a & 1, ctl)) return false;
+            ++items_a;
+            fence_after();
+            if (elect_one()) {
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    const uint32_t off = (kk / 4) * L::kSlabQ + (kk % 4) * 32;
+                    cp_128x256b(tmem + L::colQ + kk * 8, smem_desc(sbase + L::offQ + off, 16, 1024));
+                    cp_128x256b(tmem + L::colDO + kk * 8, smem_desc(sbase + L::offQ + L::kQBytes + off, 16, 1024));
+                }
+                commit(bar(QD_EMPTY));
+            }
+            __syncwarp();
+            return true;
+        };
+        auto scores = [&] {                                       // one lane
+            const uint32_t st = ua % L::kStages, buf = (ua & 1) * kKeys;
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk)
+                mma_ts(tmem + L::colS + buf, tmem + L::colQ + kk * 8,
+                       smem_desc(sbase + L::offK + st * L::kTileBytes + (kk / 4) * L::kSlab + (kk % 4) * 32, 16, 1024),
+                       idesc_s, kk > 0);
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk)
+                mma_ts(tmem + L::colDP + buf, tmem + L::colDO + kk * 8,
+                       smem_desc(sbase + L::offV + st * L::kTileBytes + (kk / 4) * L::kSlab + (kk % 4) * 32, 16, 1024),
+                       idesc_s, kk > 0);
+            commit(bar(S_FULL + (ua & 1)));
+            commit(bar(V_EMPTY + st));
+            if (ahead.last()) commit(bar(AB_FREE));
+        };
+        for (int i = 0; i < 2 && ahead.ok && (ok = ready()); ++i) {
+            fence_after();
+            if (elect_one()) scores();
+            __syncwarp();
+            ++ua;
+            ahead.next(prm);
+        }
+        for (; cur.ok && ok; cur.next(prm), ++uc) {
+            if (ahead.ok && !(ok = ready())) break;
+            // dQ of the item before this one has been read
+            if (cur.t == 0 && items_c++ > 0 && !(ok = warp_wait<kEvery>(bar(DQ_FREE), items_c & 1, ctl))) break;
+            if (!(ok = warp_wait<kEvery>(bar(DS_FULL + (uc & 1)), (uc >> 1) & 1, ctl))) break;
+            fence_after();
+            if (elect_one()) {
+                const uint32_t st = uc % L::kStages;
+#pragma unroll
+                for (int kk = 0; kk < kKeys / 16; ++kk)
+                    mma_ts(tmem + L::colDQ, tmem + L::colS + (uc & 1) * kKeys + kk * 8,
+                           smem_desc(sbase + L::offK + st * L::kTileBytes + kk * 16 * 128, L::kSlab, 1024), idesc_dq,
+                           cur.t > 0 || kk > 0);
+                commit(bar(K_EMPTY + st));
+                if (cur.last()) commit(bar(DQ_DONE));
+                if (ahead.ok) scores();
+            }
+            __syncwarp();
+            if (ahead.ok) {
+                ++ua;
+                ahead.next(prm);
+            }
+        }
+        if (!ok && lane == 0) { ctl->abort = 1; record_error(prm.err, BSA_EDEVICE, -3); }
+        if (elect_one()) {
+            commit(bar(DRAIN));
+            mbar_drain(bar(DRAIN), 0);
+        }
+        __syncwarp();
+    } else if (warp == kMmaWarp + 1) {
+        // K ring.  dQ += dS K: rows of states that do not count become zeros (0 * NaN is NaN)
+        uint32_t u = 0, raw = 0;
+        DqWalk w;
+        for (w.seek(prm); w.ok; w.next(prm), ++u) {
+            const int st = u % L::kStages;
+            if (u >= L::kStages && !(ok = warp_sleep<kEvery>(bar(K_EMPTY + st), (u / L::kStages - 1) & 1, ctl))) break;
+            uint32_t bits[2];
+            const bool all = prm.keys.bits(w.it.b, w.it.len, w.t * kKeys, lane, bits);
+            const bool fix = !all && (prm.keys.key_mask || w.it.len < prm.keys.M);
+            const uint32_t full = bar(fix ? K_RAW : K_FULL + st), dst = sbase + L::offK + st * L::kTileBytes;
+            if (lane == 0) {
+                mbar_expect_tx(full, L::kTileBytes);
+                for (int s = 0; s < D / 64; ++s)
+                    tma_load_4d(dst + s * L::kSlab, &tmK, s * 64, w.t * kKeys, w.it.h / prm.G, w.it.b, full);
+            }
+            if (fix) {
+                if (!warp_wait<kEvery>(full, raw & 1, ctl)) {
+                    mbar_drain(full, raw & 1);
+                    ok = false;
+                    break;
+                }
+                ++raw;
+                for (int i = 0; i < kKeys; ++i)
+                    if (!(bits[i / 32] >> (i % 32) & 1) && lane < D / 8)
+                        *reinterpret_cast<uint4*>(smem + (dst - sbase) + (lane / 8) * L::kSlab + i * 128 +
+                                                  (lane % 8) * 16) = make_uint4(0, 0, 0, 0);
+                fence_proxy_async();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(K_FULL + st));
+            }
+        }
+        if (!ok && lane == 0) { ctl->abort = 1; record_error(prm.err, BSA_EDEVICE, -1); }
+        for (uint32_t st = 0; st < L::kStages; ++st)
+            if (u > st) mbar_drain(bar(K_FULL + st), ((u - 1 - st) / L::kStages) & 1);
+    } else if (warp == kMmaWarp + 2) {
+        if (lane == 0) {
+            uint32_t u = 0;
+            DqWalk w;
+            for (w.seek(prm); w.ok; w.next(prm), ++u) {
+                const int st = u % L::kStages;
+                if (u >= L::kStages && !(ok = mbar_sleep<kEvery>(bar(V_EMPTY + st), (u / L::kStages - 1) & 1, ctl))) break;
+                mbar_expect_tx(bar(V_FULL + st), L::kTileBytes);
+                for (int s = 0; s < D / 64; ++s)
+                    tma_load_4d(sbase + L::offV + st * L::kTileBytes + s * L::kSlab, &tmV, s * 64, w.t * kKeys,
+                                w.it.h / prm.G, w.it.b, bar(V_FULL + st));
+            }
+            if (!ok) { ctl->abort = 1; record_error(prm.err, BSA_EDEVICE, -2); }
+            for (uint32_t st = 0; st < L::kStages; ++st)
+                if (u > st) mbar_drain(bar(V_FULL + st), ((u - 1 - st) / L::kStages) & 1);
+        }
+    } else if (warp == kMmaWarp + 3) {
+        if (lane == 0) {
+            uint32_t n = 0;
+            DqWalk w;
+            for (w.seek(prm); w.ok; w.next_item(prm), ++n) {
+                if (n > 0 && !(ok = mbar_sleep<kEvery>(bar(QD_EMPTY), (n - 1) & 1, ctl))) break;
+                mbar_expect_tx(bar(QD_FULL), 2 * L::kQBytes);
+                for (int s = 0; s < D / 64; ++s) {
+                    tma_load_4d(sbase + L::offQ + s * L::kSlabQ, &tmQ, s * 64, w.it.tile * kTile, w.it.h, w.it.b, bar(QD_FULL));
+                    tma_load_4d(sbase + L::offQ + L::kQBytes + s * L::kSlabQ, &tmDO, s * 64, w.it.tile * kTile, w.it.h,
+                                w.it.b, bar(QD_FULL));
+                }
+            }
+            if (!ok) { ctl->abort = 1; record_error(prm.err, BSA_EDEVICE, -6); }
+            if (n > 0) mbar_drain(bar(QD_FULL), (n - 1) & 1);
+        }
+    } else if (warp < kRowWarp) {
+        // ------------------------------------------------------------------ softmax
+        const int g = warp / 4, quad = warp & 3;
+        const uint32_t ts = tmem + ((uint32_t)(32 * quad) << 16) + L::colS + g * kKeys, tp = ts - L::colS + L::colDP;
+        uint32_t u = 0, ni = 0;
+        DqItem it;
+        for (int k = 0; ok && item_at(prm, k, it); ++k) {
+            if (it.nt == 0) continue;
+            if (!(ok = warp_wait<kEvery>(bar(ROWS_FULL + (ni & 1)), (ni >> 1) & 1, ctl))) break;
+            const float* rv = row_vals + (ni & 1) * 2 * kTile + 32 * quad + lane;
+            const float neg_lse = -rv[0], neg_d = -rv[kTile];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(ROWS_EMPTY + (ni & 1)));
+            ++ni;
+            for (int t = 0; t < it.nt; ++t, ++u) {
+                if ((int)(u & 1) != g) continue;
+                uint32_t bits[2];
+                const bool all = prm.keys.bits(it.b, it.len, t * kKeys, lane, bits);
+                if (!(ok = warp_wait<kEvery>(bar(S_FULL + g), (u >> 1) & 1, ctl))) break;
+                fence_after();
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    uint32_t sv[32], dv[32], pk[16];
+                    tmem_ld32(ts + c * 32, sv);
+                    tmem_ld32(tp + c * 32, dv);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 32; e += 2) {
+                        float x0, x1, d0, d1;
+                        ffma2(x0, x1, __uint_as_float(sv[e]), __uint_as_float(sv[e + 1]), prm.scale_log2, prm.scale_log2,
+                              neg_lse, neg_lse);
+                        fadd2(d0, d1, __uint_as_float(dv[e]), __uint_as_float(dv[e + 1]), neg_d, neg_d);
+                        const float p0 = ex2_mufu(x0), p1 = ex2_mufu(x1);
+                        fmul2(d0, d1, d0, d1, p0, p1);
+                        pk[e / 2] = pack_bf16(d0, d1);
+                    }
+                    if (!all) {
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            const uint32_t on = bits[c] >> (2 * e);
+                            pk[e] &= (on & 1 ? 0xffffu : 0u) | (on & 2 ? 0xffff0000u : 0u);
+                        }
+                    }
+                    tmem_st16(ts + c * 16, pk);
+                }
+                tmem_wait_st();
+                fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(DS_FULL + g));
+            }
+        }
+        if (!ok) { ctl->abort = 1; record_error(prm.err, BSA_EDEVICE, -4); }
+        tmem_wait_st();
+        tmem_wait_ld();
+    } else {
+        // --------------------------------------------- rows: D ahead of the item, dQ behind it
+        const int quad = warp & 3, r = 32 * quad + lane;
+        const uint32_t tq = tmem + ((uint32_t)(32 * quad) << 16) + L::colDQ;
+        unsigned char* stage = smem + L::offOut + quad * 4096;
+        const unsigned char* sdo = smem + L::offQ + L::kQBytes;
+        uint32_t nr = 0, nd = 0;
+        auto rows = [&](const DqItem& it) {
+            if (!warp_sleep<kEvery>(bar(QD_FULL), nr & 1, ctl)) return false;
+            if (nr >= 2 && !warp_sleep<kEvery>(bar(ROWS_EMPTY + (nr & 1)), ((nr >> 1) - 1) & 1, ctl)) return false;
+            const int n = it.tile * kTile + r;
+            float d = 0.f, lse2 = 0.f;
+            if (n < prm.N) {
+                const uint4* orow = reinterpret_cast<const uint4*>(prm.o + (((int64_t)it.b * prm.N + n) * prm.H + it.h) * D);
+#pragma unroll 4
+                for (int c = 0; c < D / 8; ++c)
+                    d += dot8(__ldg(orow + c), *reinterpret_cast<const uint4*>(sdo + swizzled(r, c, L::kSlabQ)));
+                const int64_t i = ((int64_t)it.b * prm.H + it.h) * prm.N + n;
+                const float l = prm.lse[i];
+                lse2 = l == -INFINITY ? 0.f : l * kLog2e;             // no valid state: every key is masked
+                prm.dsum[i] = d;
+            }
+            float* rv = row_vals + (nr & 1) * 2 * kTile + r;
+            rv[0] = lse2;
+            rv[kTile] = d;
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(bar(ROWS_FULL + (nr & 1)));
+                mbar_arrive(bar(QD_EMPTY));
+            }
+            ++nr;
+            return true;
+        };
+        DqWalk pre;
+        pre.seek(prm);
+        if (pre.ok) {
+            ok = rows(pre.it);
+            pre.next_item(prm);
+        }
+        DqItem it;
+        for (int k = 0; ok && item_at(prm, k, it); ++k) {
+            if (it.nt > 0) {
+                if (pre.ok) {                                         // the next item's D before this one's dQ
+                    if (!(ok = rows(pre.it))) break;
+                    pre.next_item(prm);
+                }
+                if (!(ok = warp_sleep<kEvery>(bar(DQ_DONE), nd & 1, ctl))) break;
+                ++nd;
+                fence_after();
+            }
+            const int row0 = it.tile * kTile + 32 * quad;
+#pragma unroll
+            for (int s = 0; s < D / 64; ++s) {
+                if (lane == 0) bulk_wait_read();
+                __syncwarp();
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    uint32_t v[32];
+                    if (it.nt > 0) {
+                        tmem_ld32(tq + s * 64 + c * 32, v);
+                        tmem_wait_ld();
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) v[e] = 0u;
+                    }
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        uint4 w;
+                        w.x = pack_bf16(__uint_as_float(v[8 * e + 0]) * prm.scale, __uint_as_float(v[8 * e + 1]) * prm.scale);
+                        w.y = pack_bf16(__uint_as_float(v[8 * e + 2]) * prm.scale, __uint_as_float(v[8 * e + 3]) * prm.scale);
+                        w.z = pack_bf16(__uint_as_float(v[8 * e + 4]) * prm.scale, __uint_as_float(v[8 * e + 5]) * prm.scale);
+                        w.w = pack_bf16(__uint_as_float(v[8 * e + 6]) * prm.scale, __uint_as_float(v[8 * e + 7]) * prm.scale);
+                        *reinterpret_cast<uint4*>(stage + swizzled(lane, 4 * c + e, 0)) = w;
+                    }
+                }
+                if (it.nt > 0 && s == D / 64 - 1) {
+                    fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(DQ_FREE));
+                }
+                fence_proxy_async();
+                __syncwarp();
+                if (lane == 0 && row0 < prm.N) {
+                    tma_store_4d(&tmDQ, smem_u32(stage), s * 64, row0, it.h, it.b);
+                    bulk_commit();
+                }
+            }
+        }
+        if (!ok) { ctl->abort = 1; record_error(prm.err, BSA_EDEVICE, -5); }
+        tmem_wait_ld();
+        if (lane == 0) bulk_wait();
+    }
+    end_cta(tmem);
+}
+
+// -------------------------------------------------------------------- key side
+// warps 0-7 softmax, 8-11 dK and dV to memory, 12 MMA, 13 Q / dO ring with the
+// rows' lse and D, 14 K and V.  An item: a key tile of one key head and a share
+// of the (query head, 64-token) steps that read it.
+struct DkvP {
+    Keys keys;
+    const float *lse, *dsum;
+    float* part;                     // [2: dK, dV][chunks][B, M, Hkv, D], or null: dk, dv hold the result
+    __nv_bfloat16 *dk, *dv;
+    int32_t* err;
+    int N, H, G, B, Hkv, key_tiles, chunks, nq, items;
+    int64_t part_stride;             // floats of one chunk: B * M * Hkv * D
+    float scale, scale_log2;
+    unsigned long long wait_ns;
+};
+
+template <int D>
+struct DkvSmem {
+    static constexpr int kSlab = kKeys * 128, kSlabK = kTile * 128;
+    static constexpr int kTileBytes = kKeys * D * 2, kKBytes = kTile * D * 2;
+    static constexpr int kStages = 4;
+    static constexpr int offK = 0;                                 // K, V
+    static constexpr int offQ = offK + 2 * kKBytes;                // stages of Q, dO
+    static constexpr int offRows = offQ + kStages * 2 * kTileBytes;   // stages of float lse, D [64]
+    static constexpr int offBar = offRows + kStages * 2 * kKeys * 4;
+    static constexpr int offMisc = offBar + 32 * 8;
+    static constexpr int kAlloc = offMisc + 64 + 1024;
+    static constexpr uint32_t colS = 0, colDP = 128, colDV = 256, colDK = 384;
+};
+
+struct DkvItem {
+    int b, hk, kt, chunk, len, beg, end;      // steps [beg, end); none if the tile has no valid state
+};
+__device__ __forceinline__ bool item_at(const DkvP& p, int k, DkvItem& it) {
+    int idx = k * gridDim.x + blockIdx.x;
+    if (idx >= p.items) return false;
+    it.kt = idx % p.key_tiles;
+    idx /= p.key_tiles;
+    it.chunk = idx % p.chunks;
+    idx /= p.chunks;
+    it.hk = idx % p.Hkv;
+    it.b = idx / p.Hkv;
+    it.len = p.keys.count(it.b);
+    const int64_t steps = (int64_t)p.G * p.nq;
+    it.beg = (int)(steps * it.chunk / p.chunks);
+    it.end = it.kt * kTile < it.len ? (int)(steps * (it.chunk + 1) / p.chunks) : it.beg;
+    return true;
+}
+struct DkvWalk {
+    DkvItem it;
+    int k = 0, s = 0;
+    bool ok;
+    __device__ __forceinline__ void seek(const DkvP& p) {
+        while ((ok = item_at(p, k, it)) && it.end == it.beg) ++k;
+        s = it.beg;
+    }
+    __device__ __forceinline__ void next(const DkvP& p) {
+        if (++s < it.end) return;
+        next_item(p);
+    }
+    __device__ __forceinline__ void next_item(const DkvP& p) {
+        ++k;
+        seek(p);
+    }
+    __device__ __forceinline__ bool first() const { return s == it.beg; }
+    __device__ __forceinline__ bool last() const { return s == it.end - 1; }
+};
+
+template <int D, uint32_t kEvery>
+__global__ void __launch_bounds__(kThreads, 1)
+k_cross_dkv(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+            const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmDO, const DkvP prm) {
+    using L = DkvSmem<D>;
+    enum {
+        KV_FULL = 0, KV_EMPTY, S_FULL, PD_FULL = S_FULL + 2, ACC_DONE = PD_FULL + 2, ACC_FREE, DRAIN, ST_FULL,
+        ST_EMPTY = ST_FULL + L::kStages, kBars = ST_EMPTY + L::kStages
+    };
+    static_assert(kBars <= 32, "barrier slots");
+    extern __shared__ __align__(1024) unsigned char smem_raw[];
+    unsigned char* smem = reinterpret_cast<unsigned char*>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t sbase = smem_u32(smem);
+    auto bar = [&](int i) { return sbase + L::offBar + 8u * (uint32_t)i; };
+    volatile WaitCtl* ctl = reinterpret_cast<volatile WaitCtl*>(smem + L::offMisc);
+    float* row_vals = reinterpret_cast<float*>(smem + L::offRows);
+    const uint32_t tmem = begin_cta<kBars>(bar(0), ctl, reinterpret_cast<uint32_t*>(smem + L::offMisc + 16), prm.wait_ns,
+                                           [](int i) -> uint32_t {
+                                               return (i >= PD_FULL && i < PD_FULL + 2) || i == ACC_FREE ? 4 : 1;
+                                           });
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
+    bool ok = true;
+
+    if (warp == kMmaWarp) {
+        constexpr uint32_t idesc_s = instr_desc(kKeys, 0), idesc_g = instr_desc(D, 1);
+        uint32_t ua = 0, uc = 0, items_a = 0, items_c = 0;
+        DkvWalk cur, ahead;
+        cur.seek(prm);
+        ahead = cur;
+        auto ready = [&] {
+            if (!warp_wait<kEvery>(bar(ST_FULL + ua % L::kStages), (ua / L::kStages) & 1, ctl)) return false;
+            return !ahead.first() || warp_wait<kEvery>(bar(KV_FULL), items_a++ & 1, ctl);
+        };
+        auto scores = [&] {                                       // one lane
+            const uint32_t buf = (ua & 1) * kKeys, q = sbase + L::offQ + ua % L::kStages * 2 * L::kTileBytes;
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk)
+                mma_ss(tmem + L::colS + buf, smem_desc(sbase + L::offK + (kk / 4) * L::kSlabK + (kk % 4) * 32, 16, 1024),
+                       smem_desc(q + (kk / 4) * L::kSlab + (kk % 4) * 32, 16, 1024), idesc_s, kk > 0);
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk)
+                mma_ss(tmem + L::colDP + buf,
+                       smem_desc(sbase + L::offK + L::kKBytes + (kk / 4) * L::kSlabK + (kk % 4) * 32, 16, 1024),
+                       smem_desc(q + L::kTileBytes + (kk / 4) * L::kSlab + (kk % 4) * 32, 16, 1024), idesc_s, kk > 0);
+            commit(bar(S_FULL + (ua & 1)));
+            if (ahead.last()) commit(bar(KV_EMPTY));
+        };
+        for (int i = 0; i < 2 && ahead.ok && (ok = ready()); ++i) {
+            fence_after();
+            if (elect_one()) scores();
+            __syncwarp();
+            ++ua;
+            ahead.next(prm);
+        }
+        for (; cur.ok && ok; cur.next(prm), ++uc) {
+            if (ahead.ok && !(ok = ready())) break;
+            if (cur.first() && items_c++ > 0 && !(ok = warp_wait<kEvery>(bar(ACC_FREE), items_c & 1, ctl))) break;
+            if (!(ok = warp_wait<kEvery>(bar(PD_FULL + (uc & 1)), (uc >> 1) & 1, ctl))) break;
+            fence_after();
+            if (elect_one()) {
+                const uint32_t st = uc % L::kStages, q = sbase + L::offQ + st * 2 * L::kTileBytes, buf = (uc & 1) * kKeys;
+#pragma unroll
+                for (int kk = 0; kk < kKeys / 16; ++kk)
+                    mma_ts(tmem + L::colDV, tmem + L::colS + buf + kk * 8,
+                           smem_desc(q + L::kTileBytes + kk * 16 * 128, L::kSlab, 1024), idesc_g, !cur.first() || kk > 0);
+#pragma unroll
+                for (int kk = 0; kk < kKeys / 16; ++kk)
+                    mma_ts(tmem + L::colDK, tmem + L::colDP + buf + kk * 8, smem_desc(q + kk * 16 * 128, L::kSlab, 1024),
+                           idesc_g, !cur.first() || kk > 0);
+                commit(bar(ST_EMPTY + st));
+                if (cur.last()) commit(bar(ACC_DONE));
+                if (ahead.ok) scores();
+            }
+            __syncwarp();
+            if (ahead.ok) {
+                ++ua;
+                ahead.next(prm);
+            }
+        }
+        if (!ok && lane == 0) { ctl->abort = 1; record_error(prm.err, BSA_EDEVICE, -3); }
+        if (elect_one()) {
+            commit(bar(DRAIN));
+            mbar_drain(bar(DRAIN), 0);
+        }
+        __syncwarp();
+    } else if (warp == kMmaWarp + 1) {
+        uint32_t u = 0;
+        DkvWalk w;
+        for (w.seek(prm); w.ok; w.next(prm), ++u) {
+            const int st = u % L::kStages;
+            const int h = w.it.hk * prm.G + w.s / prm.nq, q0 = w.s % prm.nq * kKeys;
+            float l[2], d[2];                            // rows past N: lse = inf, so P is 0
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int n = q0 + 32 * i + lane;
+                const int64_t at = ((int64_t)w.it.b * prm.H + h) * prm.N + n;
+                l[i] = n < prm.N ? prm.lse[at] * kLog2e : INFINITY;
+                d[i] = n < prm.N ? prm.dsum[at] : 0.f;
+            }
+            if (u >= L::kStages && !(ok = warp_sleep<kEvery>(bar(ST_EMPTY + st), (u / L::kStages - 1) & 1, ctl))) break;
+            float* rv = row_vals + st * 2 * kKeys + lane;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                rv[32 * i] = l[i] == -INFINITY ? INFINITY : l[i];
+                rv[kKeys + 32 * i] = d[i];
+            }
+            __syncwarp();
+            if (lane == 0) {
+                const uint32_t dst = sbase + L::offQ + st * 2 * L::kTileBytes;
+                mbar_expect_tx(bar(ST_FULL + st), 2 * L::kTileBytes);
+                for (int s = 0; s < D / 64; ++s) {
+                    tma_load_4d(dst + s * L::kSlab, &tmQ, s * 64, q0, h, w.it.b, bar(ST_FULL + st));
+                    tma_load_4d(dst + L::kTileBytes + s * L::kSlab, &tmDO, s * 64, q0, h, w.it.b, bar(ST_FULL + st));
+                }
+            }
+        }
+        if (!ok && lane == 0) { ctl->abort = 1; record_error(prm.err, BSA_EDEVICE, -1); }
+        for (uint32_t st = 0; st < L::kStages; ++st)
+            if (u > st) mbar_drain(bar(ST_FULL + st), ((u - 1 - st) / L::kStages) & 1);
+    } else if (warp == kMmaWarp + 2) {
+        if (lane == 0) {
+            uint32_t n = 0;
+            DkvWalk w;
+            for (w.seek(prm); w.ok; w.next_item(prm), ++n) {
+                if (n > 0 && !(ok = mbar_sleep<kEvery>(bar(KV_EMPTY), (n - 1) & 1, ctl))) break;
+                mbar_expect_tx(bar(KV_FULL), 2 * L::kKBytes);
+                for (int s = 0; s < D / 64; ++s) {
+                    tma_load_4d(sbase + L::offK + s * L::kSlabK, &tmK, s * 64, w.it.kt * kTile, w.it.hk, w.it.b, bar(KV_FULL));
+                    tma_load_4d(sbase + L::offK + L::kKBytes + s * L::kSlabK, &tmV, s * 64, w.it.kt * kTile, w.it.hk, w.it.b,
+                                bar(KV_FULL));
+                }
+            }
+            if (!ok) { ctl->abort = 1; record_error(prm.err, BSA_EDEVICE, -2); }
+            if (n > 0) mbar_drain(bar(KV_FULL), (n - 1) & 1);
+        }
+    } else if (warp < kRowWarp) {
+        // ------------------------------------------------------------------ softmax
+        const int g = warp / 4, quad = warp & 3;
+        const uint32_t ts = tmem + ((uint32_t)(32 * quad) << 16) + L::colS + g * kKeys, tp = ts - L::colS + L::colDP;
+        uint32_t u = 0;
+        DkvWalk w;
+        w.seek(prm);
+        for (; w.ok; w.next_item(prm)) {
+            const int j = w.it.kt * kTile + 32 * quad + lane;         // this thread's key
+            const bool on = j < w.it.len && (!prm.keys.key_mask || prm.keys.key_mask[(int64_t)w.it.b * prm.keys.M + j]);
+            for (int s = w.it.beg; s < w.it.end; ++s, ++u) {
+                if ((int)(u & 1) != g) continue;
+                const int st = u % L::kStages;
+                if (!(ok = warp_wait<kEvery>(bar(ST_FULL + st), (u / L::kStages) & 1, ctl))) break;
+                if (!(ok = warp_wait<kEvery>(bar(S_FULL + g), (u >> 1) & 1, ctl))) break;
+                fence_after();
+                const float* rv = row_vals + st * 2 * kKeys;
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    uint32_t sv[32], dv[32], pk[16], dk[16];
+                    tmem_ld32(ts + c * 32, sv);
+                    tmem_ld32(tp + c * 32, dv);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4) {
+                        const float4 l4 = *reinterpret_cast<const float4*>(rv + c * 32 + e);
+                        const float4 d4 = *reinterpret_cast<const float4*>(rv + kKeys + c * 32 + e);
+                        const float l[4] = {l4.x, l4.y, l4.z, l4.w}, d[4] = {d4.x, d4.y, d4.z, d4.w};
+#pragma unroll
+                        for (int f = 0; f < 4; f += 2) {
+                            float x0, x1, d0, d1;
+                            ffma2(x0, x1, __uint_as_float(sv[e + f]), __uint_as_float(sv[e + f + 1]), prm.scale_log2,
+                                  prm.scale_log2, -l[f], -l[f + 1]);
+                            fadd2(d0, d1, __uint_as_float(dv[e + f]), __uint_as_float(dv[e + f + 1]), -d[f], -d[f + 1]);
+                            const float p0 = ex2_mufu(x0), p1 = ex2_mufu(x1);
+                            fmul2(d0, d1, d0, d1, p0, p1);
+                            pk[(e + f) / 2] = pack_bf16(p0, p1);
+                            dk[(e + f) / 2] = pack_bf16(d0, d1);
+                        }
+                    }
+                    if (!on) {
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) pk[e] = dk[e] = 0u;
+                    }
+                    tmem_st16(ts + c * 16, pk);
+                    tmem_st16(tp + c * 16, dk);
+                }
+                tmem_wait_st();
+                fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(PD_FULL + g));
+            }
+            if (!ok) break;
+        }
+        if (!ok) { ctl->abort = 1; record_error(prm.err, BSA_EDEVICE, -4); }
+        tmem_wait_st();
+        tmem_wait_ld();
+    } else if (warp < kMmaWarp) {
+        // ------------------------------------------------------------ dK, dV of an item
+        const int quad = warp & 3;
+        const uint32_t tl = tmem + ((uint32_t)(32 * quad) << 16);
+        uint32_t nd = 0;
+        DkvItem it;
+        for (int k = 0; ok && item_at(prm, k, it); ++k) {
+            const bool work = it.end > it.beg;
+            if (!work && prm.part) continue;                          // the sum leaves this tile out
+            const int j = it.kt * kTile + 32 * quad + lane;
+            if (work) {
+                if (!(ok = warp_sleep<kEvery>(bar(ACC_DONE), nd & 1, ctl))) break;
+                ++nd;
+                fence_after();
+            }
+            const int64_t at = (((int64_t)it.b * prm.keys.M + j) * prm.Hkv + it.hk) * D;
+#pragma unroll 1
+            for (int c = 0; c < 2 * D / 32; ++c) {
+                const bool is_v = c < D / 32;
+                const int col = (is_v ? c : c - D / 32) * 32;
+                uint32_t v[32];
+                if (work) {
+                    tmem_ld32(tl + (is_v ? L::colDV : L::colDK) + col, v);
+                    tmem_wait_ld();
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) v[e] = 0u;
+                }
+                if (j >= prm.keys.M) continue;
+                if (prm.part) {
+                    float4* dst = reinterpret_cast<float4*>(prm.part + ((is_v ? prm.chunks : 0) + it.chunk) * prm.part_stride +
+                                                            at + col);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        dst[e] = make_float4(__uint_as_float(v[4 * e]), __uint_as_float(v[4 * e + 1]),
+                                             __uint_as_float(v[4 * e + 2]), __uint_as_float(v[4 * e + 3]));
+                } else {
+                    const float f = is_v ? 1.f : prm.scale;
+                    uint4* dst = reinterpret_cast<uint4*>((is_v ? prm.dv : prm.dk) + at + col);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        uint4 w;
+                        w.x = pack_bf16(__uint_as_float(v[8 * e + 0]) * f, __uint_as_float(v[8 * e + 1]) * f);
+                        w.y = pack_bf16(__uint_as_float(v[8 * e + 2]) * f, __uint_as_float(v[8 * e + 3]) * f);
+                        w.z = pack_bf16(__uint_as_float(v[8 * e + 4]) * f, __uint_as_float(v[8 * e + 5]) * f);
+                        w.w = pack_bf16(__uint_as_float(v[8 * e + 6]) * f, __uint_as_float(v[8 * e + 7]) * f);
+                        dst[e] = w;
+                    }
+                }
+            }
+            if (work) {
+                fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(ACC_FREE));
+            }
+        }
+        if (!ok) { ctl->abort = 1; record_error(prm.err, BSA_EDEVICE, -5); }
+        tmem_wait_ld();
+    }
+    end_cta(tmem);
+}
+
+// dK (scaled) and dV from the shares, in share order; tiles without a valid state are zero.
+__global__ void k_cross_dkv_sum(const DkvP prm, int D) {
+    const int64_t i4 = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+    if (i4 * 4 >= prm.part_stride) return;
+    const bool is_v = blockIdx.y != 0;
+    const int64_t row = i4 * 4 / ((int64_t)prm.Hkv * D), b = row / prm.keys.M;
+    const int j = (int)(row - b * prm.keys.M);
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (j / kTile * kTile < prm.keys.count((int)b)) {
+        const float* src = prm.part + (is_v ? prm.chunks * prm.part_stride : 0) + i4 * 4;
+        for (int c = 0; c < prm.chunks; ++c) {
+            const float4 v = __ldcs(reinterpret_cast<const float4*>(src + c * prm.part_stride));
+            s.x += v.x;
+            s.y += v.y;
+            s.z += v.z;
+            s.w += v.w;
+        }
+    }
+    const float f = is_v ? 1.f : prm.scale;
+    reinterpret_cast<uint2*>(is_v ? prm.dv : prm.dk)[i4] = make_uint2(pack_bf16(s.x * f, s.y * f), pack_bf16(s.z * f, s.w * f));
+}
+
+// Shares of the query steps for one key tile: enough items to fill the SMs evenly, each share at least 8 steps.
+int share_count(const bsa_plan& p, int64_t M, int Hkv) {
+    const int64_t tiles = (int64_t)p.B * Hkv * ((M + kTile - 1) / kTile);
+    const int64_t steps = (int64_t)(p.H / Hkv) * ((p.N + kKeys - 1) / kKeys);
+    int best = 1;
+    double best_cost = 1e300;
+    for (int c = 1; c <= 64 && (c == 1 || steps / c >= 8); ++c) {
+        const int64_t waves = (tiles * c + p.num_sms - 1) / p.num_sms;
+        // in steps of one SM: a share, its start and end (about 3 steps), and a little for the sum's traffic
+        const double cost = (double)waves * ((double)steps / c + 3.0) + (c > 1 ? 0.02 * tiles * c : 0.0);
+        if (cost < best_cost) {
+            best_cost = cost;
+            best = c;
+        }
+    }
+    return best;
+}
+
+template <int D, uint32_t kEvery>
+cudaError_t launch_t(const bsa_plan& p, const CrossArgs& a, const DqP& pq, const DkvP& pk, const void* d_o, void* dq,
+                     cudaStream_t s) {
+    CUtensorMap mq, mk, mv, mg, mo;
+    int64_t so[3];
+    dense_strides(so, p.N, p.H, D);
+    if (!make_map_4d(&mq, a.q, p.B, p.N, p.H, D, a.st, kTile) || !make_map_4d(&mk, a.k, p.B, a.M, a.Hkv, D, a.st + 3, kKeys) ||
+        !make_map_4d(&mv, a.v, p.B, a.M, a.Hkv, D, a.st + 6, kKeys) || !make_map_4d(&mg, d_o, p.B, p.N, p.H, D, so, kTile) ||
+        !make_map_4d(&mo, dq, p.B, p.N, p.H, D, so, 32))
+        return cudaErrorInvalidValue;
+    cudaError_t e = cudaFuncSetAttribute(k_cross_dq<D, kEvery>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         DqSmem<D>::kAlloc);
+    if (e != cudaSuccess) return e;
+    k_cross_dq<D, kEvery><<<std::min(p.num_sms, pq.items), kThreads, DqSmem<D>::kAlloc, s>>>(mq, mk, mv, mg, mo, pq);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+
+    if (!make_map_4d(&mq, a.q, p.B, p.N, p.H, D, a.st, kKeys) || !make_map_4d(&mk, a.k, p.B, a.M, a.Hkv, D, a.st + 3, kTile) ||
+        !make_map_4d(&mv, a.v, p.B, a.M, a.Hkv, D, a.st + 6, kTile) || !make_map_4d(&mg, d_o, p.B, p.N, p.H, D, so, kKeys))
+        return cudaErrorInvalidValue;
+    e = cudaFuncSetAttribute(k_cross_dkv<D, kEvery>, cudaFuncAttributeMaxDynamicSharedMemorySize, DkvSmem<D>::kAlloc);
+    if (e != cudaSuccess) return e;
+    k_cross_dkv<D, kEvery><<<std::min(p.num_sms, pk.items), kThreads, DkvSmem<D>::kAlloc, s>>>(mq, mk, mv, mg, pk);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    if (pk.part) {
+        k_cross_dkv_sum<<<dim3((unsigned)((pk.part_stride / 4 + 255) / 256), 2), 256, 0, s>>>(pk, D);
+        e = cudaGetLastError();
+    }
+    return e;
+}
+
+template <int D>
+cudaError_t launch_d(const bsa_plan& p, const CrossArgs& a, const DqP& pq, const DkvP& pk, const void* d_o, void* dq,
+                     cudaStream_t s) {
+    // a wait limit below a millisecond: the variant that checks it at every probe
+    return p.wait_ns < 1000000ull ? launch_t<D, 0>(p, a, pq, pk, d_o, dq, s) : launch_t<D, 1023>(p, a, pq, pk, d_o, dq, s);
+}
+
+size_t dsum_bytes(const bsa_plan& p) { return align_up((size_t)p.B * p.H * p.N * sizeof(float)); }
+
+}  // namespace
+
+size_t cross_bwd_ws_bytes(const bsa_plan& p, int64_t M, int Hkv) {
+    const int c = M > 0 ? share_count(p, M, Hkv) : 1;
+    const size_t part = (size_t)p.B * M * Hkv * p.d * sizeof(float);
+    return dsum_bytes(p) + (c > 1 ? align_up(2 * c * part) : 0);
+}
+
+cudaError_t launch_cross_bwd_tc(const bsa_plan& p, const CrossArgs& a, const void* o, const float* lse, const void* d_o,
+                                void* dq, void* dk, void* dv, void* ws, cudaStream_t s) {
+    DqP pq;
+    pq.keys = Keys{a.kv_len, a.key_mask, (int)a.M};
+    pq.o = (const __nv_bfloat16*)o;
+    pq.lse = lse;
+    pq.dsum = (float*)ws;
+    pq.err = p.d_err;
+    pq.N = (int)p.N;
+    pq.H = p.H;
+    pq.G = p.H / a.Hkv;
+    pq.tiles = (int)((p.N + kTile - 1) / kTile);
+    pq.items = p.B * p.H * pq.tiles;
+    pq.scale = 1.f / sqrtf((float)p.d);
+    pq.scale_log2 = kLog2e * pq.scale;
+    pq.wait_ns = p.wait_ns;
+    DkvP pk;
+    pk.keys = pq.keys;
+    pk.lse = lse;
+    pk.dsum = pq.dsum;
+    pk.chunks = share_count(p, a.M, a.Hkv);
+    pk.part = pk.chunks > 1 ? (float*)((char*)ws + dsum_bytes(p)) : nullptr;
+    pk.dk = (__nv_bfloat16*)dk;
+    pk.dv = (__nv_bfloat16*)dv;
+    pk.err = p.d_err;
+    pk.N = pq.N; pk.H = p.H; pk.G = pq.G; pk.B = p.B; pk.Hkv = a.Hkv;
+    pk.key_tiles = (int)((a.M + kTile - 1) / kTile);
+    pk.nq = (int)((p.N + kKeys - 1) / kKeys);
+    pk.items = p.B * a.Hkv * pk.key_tiles * pk.chunks;
+    pk.part_stride = (int64_t)p.B * a.M * a.Hkv * p.d;
+    pk.scale = pq.scale; pk.scale_log2 = pq.scale_log2;
+    pk.wait_ns = p.wait_ns;
+    return p.d == 128 ? launch_d<128>(p, a, pq, pk, d_o, dq, s) : launch_d<64>(p, a, pq, pk, d_o, dq, s);
+}
+
+}  // namespace bsa
