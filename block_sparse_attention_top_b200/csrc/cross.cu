@@ -164,6 +164,7 @@ size_t cross_ws_bytes(const bsa_plan& p, int64_t M, int Hkv, bool backward) {
 }
 
 cudaError_t launch_cross(const bsa_plan& p, const CrossArgs& a, void* o, float* lse, void*, cudaStream_t s) {
+    if (a.M > 0 && p.N * (p.H / a.Hkv) <= 64 && (int64_t)p.B * a.Hkv <= 65535) return launch_cross_few(p, a, o, lse, s);
     if (a.M > 0) return launch_cross_fwd_tc(p, a, o, lse, s);
     const CrossP c = cross_params(p, a);
     auto kern = p.d == 128 ? k_cross_rows<128> : k_cross_rows<64>;

@@ -124,6 +124,8 @@ inline void dense_strides(int64_t* st, int64_t rows, int64_t heads, int d) {
 // cross_fwd.cu: M > 0
 cudaError_t launch_cross_fwd_tc(const bsa_plan& p, const CrossArgs& a, void* o, float* lse, cudaStream_t s);
 
+// cross_few.cu: few query rows, M > 0
+cudaError_t launch_cross_few(const bsa_plan& p, const CrossArgs& a, void* o, float* lse, cudaStream_t s);
 // cross_bwd.cu: M > 0
 size_t cross_bwd_ws_bytes(const bsa_plan& p, int64_t M, int Hkv);
 cudaError_t launch_cross_bwd_tc(const bsa_plan& p, const CrossArgs& a, const void* o, const float* lse, const void* d_o,
