@@ -237,25 +237,49 @@ __device__ __forceinline__ void normalise(float* v, int kind, const NormP& p, co
     for (int i = 0; i < kCols; ++i) v[i] *= r;
 }
 
+// A group's parameters folded into three coefficients a channel: x_out = r x + g post(y), h = a xhat + b.
+struct Coef {
+    float g[kCols], a[kCols], b[kCols];
+};
+template <int VEC>
+__device__ __forceinline__ void load_coef(Coef& k, const NormP& p, int64_t grp, const Cols<VEC>& c, bool has_y) {
+    const int64_t gbase = grp * p.C;
+    if (has_y) {
+#pragma unroll
+        for (int i = 0; i < kCols; ++i) k.g[i] = 1.f;
+        with_param(k.g, p.post_weight, c, times);
+        if (p.gate) with_param(k.g, p.gate + gbase, c, times);
+    }
+    if (p.norm == BSA_NORM_NONE) return;
+#pragma unroll
+    for (int i = 0; i < kCols; ++i) {
+        k.a[i] = 1.f;
+        k.b[i] = 0.f;
+    }
+    with_param(k.a, p.weight, c, times);
+    with_param(k.b, p.bias, c, plus);
+    if (p.scale) {
+        with_param(k.a, p.scale + gbase, c, times1);
+        if (p.bias) with_param(k.b, p.scale + gbase, c, times1);
+    }
+    if (p.shift) with_param(k.b, p.shift + gbase, c, plus);
+}
+
 // One row: v holds x, u holds y (if any).
 template <typename TX, int VEC, bool kWarpRow>
 __device__ __forceinline__ void norm_row(const NormP& p, int64_t row, const Cols<VEC>& c, float* v, float* u, bool has_y,
-                                         TX* x_out, __nv_bfloat16* h, float* red) {
-    const int64_t base = row * p.C, gbase = row / p.group_rows * p.C;
+                                         const Coef& k, TX* x_out, __nv_bfloat16* h, float* red) {
+    const int64_t base = row * p.C;
     if (has_y) {
         if (p.post != BSA_NORM_NONE) normalise<VEC, kWarpRow>(u, p.post, p, c, red);
-        with_param(u, p.post_weight, c, times);
-        if (p.gate) with_param(u, p.gate + gbase, c, times);
 #pragma unroll
-        for (int i = 0; i < kCols; ++i) v[i] = p.res_scale * v[i] + u[i];
+        for (int i = 0; i < kCols; ++i) v[i] = fmaf(k.g[i], u[i], p.res_scale * v[i]);
         store_row(x_out + base, c, v);
     }
     if (p.norm == BSA_NORM_NONE) return;
     normalise<VEC, kWarpRow>(v, p.norm, p, c, red + 64);
-    with_param(v, p.weight, c, times);
-    with_param(v, p.bias, c, plus);
-    if (p.scale) with_param(v, p.scale + gbase, c, times1);
-    if (p.shift) with_param(v, p.shift + gbase, c, plus);
+#pragma unroll
+    for (int i = 0; i < kCols; ++i) v[i] = fmaf(k.a[i], v[i], k.b[i]);
     store_row(h + base, c, v);
 }
 
@@ -269,45 +293,11 @@ k_norm_warp(const NormP p, const TX* x, const __nv_bfloat16* y, TX* x_out, __nv_
     float v[kCols], u[kCols];
     load_row<VEC>(x + row * p.C, c, v);
     if (y) load_row<VEC>(y + row * p.C, c, u);
-    norm_row<TX, VEC, true>(p, row, c, v, u, y != nullptr, x_out, h, nullptr);
+    Coef k;
+    load_coef(k, p, row / p.group_rows, c, y != nullptr);
+    norm_row<TX, VEC, true>(p, row, c, v, u, y != nullptr, k, x_out, h, nullptr);
 }
 
-// A CTA to a row, rows in steps of the grid.
-template <typename TX, int VEC, int kStages>
-__global__ void __launch_bounds__(1024)
-k_norm_cta(const NormP p, const TX* x, const __nv_bfloat16* y, TX* x_out, __nv_bfloat16* h) {
-    extern __shared__ __align__(16) unsigned char ring[];
-    __shared__ float red[2][4 * 32];                     // rows alternate: a barrier lies between two uses
-    const Cols<VEC> c{p.C, (int)threadIdx.x, (int)blockDim.x};
-    const int x_bytes = row_pieces<TX>() * 16 * blockDim.x, stage = x_bytes + (y ? row_pieces<__nv_bfloat16>() * 16 * blockDim.x : 0);
-    auto fetch = [&](int64_t row, int st) {
-        if constexpr (VEC == 8) {
-            if (row < p.rows) {
-                fetch_row(ring + st * stage, x + row * p.C, c);
-                if (y) fetch_row(ring + st * stage + x_bytes, y + row * p.C, c);
-            }
-            fetch_commit();
-        }
-    };
-    int64_t row = blockIdx.x;
-    for (int i = 0; i < kStages - 1; ++i) fetch(row + (int64_t)i * gridDim.x, i);
-    for (int n = 0; row < p.rows; row += gridDim.x, ++n) {
-        fetch(row + (int64_t)(kStages - 1) * gridDim.x, (n + kStages - 1) % kStages);
-        float v[kCols], u[kCols];
-        if constexpr (VEC == 8) {
-            fetch_wait<kStages - 1>();
-            const unsigned char* s = ring + n % kStages * stage;
-            slot_row<TX>(s, c, v);
-            if (y) slot_row<__nv_bfloat16>(s + x_bytes, c, u);
-        } else {
-            load_row<VEC>(x + row * p.C, c, v);
-            if (y) load_row<VEC>(y + row * p.C, c, u);
-        }
-        norm_row<TX, VEC, false>(p, row, c, v, u, y != nullptr, x_out, h, red[n & 1]);
-    }
-}
-
-// ------------------------------------------------------------------ backward
 // Rows of CTA i of n: the first rows % n CTAs have one more.
 struct Ranges {
     int64_t rows;
@@ -319,6 +309,51 @@ struct Ranges {
     }
 };
 
+// A CTA to a row, a range of rows to a CTA, the coefficients of the group in registers.
+template <typename TX, int VEC, int kStages, int kThreads>
+__global__ void __launch_bounds__(kThreads, kThreads <= 320 ? 2 : 1)
+k_norm_cta(const NormP p, const Ranges rg, const TX* x, const __nv_bfloat16* y, TX* x_out, __nv_bfloat16* h) {
+    extern __shared__ __align__(16) unsigned char ring[];
+    __shared__ float red[2][4 * 32];                     // rows alternate: a barrier lies between two uses
+    const Cols<VEC> c{p.C, (int)threadIdx.x, (int)blockDim.x};
+    const int x_bytes = row_pieces<TX>() * 16 * blockDim.x, stage = x_bytes + (y ? row_pieces<__nv_bfloat16>() * 16 * blockDim.x : 0);
+    const int64_t r0 = rg.begin(blockIdx.x), r1 = rg.begin(blockIdx.x + 1);
+    auto fetch = [&](int64_t row, int st) {
+        if constexpr (VEC == 8) {
+            if (row < r1) {
+                fetch_row(ring + st * stage, x + row * p.C, c);
+                if (y) fetch_row(ring + st * stage + x_bytes, y + row * p.C, c);
+            }
+            fetch_commit();
+        }
+    };
+    for (int i = 0; i < kStages - 1; ++i) fetch(r0 + i, i);
+    Coef coef;
+    int64_t grp = r0 / p.group_rows, left = 0;           // rows of the group still to come
+    for (int64_t row = r0; row < r1; ++row) {
+        const int n = (int)(row - r0);
+        if (left == 0) {
+            grp = row / p.group_rows;
+            left = (grp + 1) * p.group_rows - row;
+            load_coef(coef, p, grp, c, y != nullptr);
+        }
+        --left;
+        fetch(row + kStages - 1, (n + kStages - 1) % kStages);
+        float v[kCols], u[kCols];
+        if constexpr (VEC == 8) {
+            fetch_wait<kStages - 1>();
+            const unsigned char* s = ring + n % kStages * stage;
+            slot_row<TX>(s, c, v);
+            if (y) slot_row<__nv_bfloat16>(s + x_bytes, c, u);
+        } else {
+            load_row<VEC>(x + row * p.C, c, v);
+            if (y) load_row<VEC>(y + row * p.C, c, u);
+        }
+        norm_row<TX, VEC, false>(p, row, c, v, u, y != nullptr, coef, x_out, h, red[n & 1]);
+    }
+}
+
+// ------------------------------------------------------------------ backward
 struct GradP {
     float *dgate, *dscale, *dshift, *dweight, *dbias, *dpost;
     float* piece;                    // [n][2][3][C]: a CTA's first and last pieces of split groups
@@ -632,11 +667,12 @@ cudaError_t fwd(const bsa_plan& p, const NormP& n, const void* x, const void* y,
     const int row_bytes = threads * kCols * (int)(sizeof(TX) + (y ? 2 : 0));
     const bool three = 3 * row_bytes <= 96 * 1024;
     const int smem = VEC == 8 ? (three ? 3 : 2) * row_bytes : 0;
-    auto kern = three || VEC == 1 ? k_norm_cta<TX, VEC, 3> : k_norm_cta<TX, VEC, 2>;
+    auto kern = threads <= 320 ? (three || VEC == 1 ? k_norm_cta<TX, VEC, 3, 320> : k_norm_cta<TX, VEC, 2, 320>)
+                               : (three || VEC == 1 ? k_norm_cta<TX, VEC, 3, 1024> : k_norm_cta<TX, VEC, 2, 1024>);
     if (smem > 48 * 1024)
         if (cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) return e;
-    const int64_t grid = std::min<int64_t>(n.rows, (int64_t)p.num_sms * ctas_per_sm(threads, 64, smem));
-    kern<<<(unsigned)grid, threads, smem, s>>>(n, xi, yi, (TX*)x_out, (__nv_bfloat16*)h);
+    const Ranges rg{n.rows, (int)std::min<int64_t>(n.rows, (int64_t)p.num_sms * ctas_per_sm(threads, threads <= 320 ? 102 : 64, smem))};
+    kern<<<rg.n, threads, smem, s>>>(n, rg, xi, yi, (TX*)x_out, (__nv_bfloat16*)h);
     return cudaGetLastError();
 }
 
