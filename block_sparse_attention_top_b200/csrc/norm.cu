@@ -112,7 +112,7 @@ struct NormP {
     const float *gate, *scale, *shift, *weight, *bias, *post_weight;
 };
 
-// A thread's channels: kCols / VEC runs of VEC, run k at (first + k * stride) * VEC.
+// A thread's channels: runs of VEC, run k at (first + k * stride) * VEC.
 template <int VEC>
 struct Cols {
     int C, first, stride;
@@ -360,167 +360,298 @@ struct GradP {
     float* wsum;                     // [n][3][C]: a CTA's sums for dweight, dbias, dpost_weight
 };
 
-constexpr int kBwdStages = 3, kRingThreads = 384;
+// Sums of 4 G values over a CTA with one barrier, through red[4 G][32] (zero where no warp writes).  Four values take
+// six shuffles to a warp's sums (each step halves what a lane still carries), and behind the barrier one 16-byte load
+// and three shuffles add 32 warps' sums of all four.
+template <int G>
+__device__ __forceinline__ void cta_sums(float* v, float* red) {
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const bool h16 = lane & 16, h8 = lane & 8;
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+        float* w = v + 4 * g;
+        float a0 = h16 ? w[2] : w[0], a1 = h16 ? w[3] : w[1];
+        a0 += __shfl_xor_sync(0xffffffffu, h16 ? w[0] : w[2], 16);
+        a1 += __shfl_xor_sync(0xffffffffu, h16 ? w[1] : w[3], 16);
+        float c = (h8 ? a1 : a0) + __shfl_xor_sync(0xffffffffu, h8 ? a0 : a1, 8);
+        c += __shfl_xor_sync(0xffffffffu, c, 4);
+        c += __shfl_xor_sync(0xffffffffu, c, 2);
+        c += __shfl_xor_sync(0xffffffffu, c, 1);
+        if ((lane & 7) == 0) red[(4 * g + lane / 8) * 32 + warp] = c;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+        const float4 f = *reinterpret_cast<const float4*>(red + (4 * g + lane / 8) * 32 + 4 * (lane & 7));
+        float s = (f.x + f.y) + (f.z + f.w);
+        s += __shfl_xor_sync(0xffffffffu, s, 1);
+        s += __shfl_xor_sync(0xffffffffu, s, 2);
+        s += __shfl_xor_sync(0xffffffffu, s, 4);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[4 * g + k] = __shfl_sync(0xffffffffu, s, 8 * k);
+    }
+}
 
-// kThreads: upper bound of the CTA size (the register budget follows from it); kToken: every token is a group
-template <typename TX, int VEC, int kThreads, bool kToken>
+// Channels a thread holds in the backward kernel: 8, or 16 where a row would need more than 1024 threads.
+constexpr int bwd_cols(int C) { return C <= 8 * 1024 ? 8 : 16; }
+constexpr int kBwdStages = 3;
+
+// kToken: every token is a group; kPost: the branch is normalised; kRing: rows come through the ring
+template <typename TX, int VEC, int NC, int kThreads, bool kToken, bool kPost, bool kRing>
 __global__ void __launch_bounds__(kThreads, 1)
 k_norm_bwd(const NormP p, const GradP g, const Ranges rg, const __nv_bfloat16* dh, const TX* dx_out,
            const TX* x_out, const __nv_bfloat16* y, TX* dx, __nv_bfloat16* dy) {
+    constexpr int R = NC / VEC;                          // runs
+    constexpr int G = kPost ? 2 : 1;
     extern __shared__ __align__(16) unsigned char ring[];
-    __shared__ float red[2][8 * 32];                     // rows alternate
-    constexpr bool kRing = VEC == 8 && kThreads <= kRingThreads;      // longer rows: the ring would not fit
+    __shared__ __align__(16) float red[2][(G + 1) * 4 * 32];          // rows alternate
+    for (int i = threadIdx.x; i < 2 * (G + 1) * 4 * 32; i += blockDim.x) red[0][i] = 0.f;
+    __syncthreads();
     const Cols<VEC> c{p.C, (int)threadIdx.x, (int)blockDim.x};
     const int64_t r0 = rg.begin(blockIdx.x), r1 = rg.begin(blockIdx.x + 1);
-    const int xb = row_pieces<TX>() * 16 * blockDim.x, hb = row_pieces<__nv_bfloat16>() * 16 * blockDim.x;
+    const bool lx = dh && p.norm == BSA_NORM_LAYER, ly = kPost && p.post == BSA_NORM_LAYER;
+
+    // ---- loads of a row's channels
+    const int xb = NC * (int)sizeof(TX) * blockDim.x, hb = NC * 2 * blockDim.x;
     const int off_h = dh ? xb : 0, off_d = off_h + (dh ? hb : 0), off_y = off_d + (dx_out ? xb : 0),
               stage = off_y + (y ? hb : 0);
+    auto fetch_one = [&](unsigned char* slot, const auto* t) {
+        constexpr int kPer = 8 * sizeof(*t) / 16;
+#pragma unroll
+        for (int k = 0; k < NC / 8; ++k)
+            if (c.in(k))
+#pragma unroll
+                for (int i = 0; i < kPer; ++i)
+                    fetch16((uint32_t)__cvta_generic_to_shared(slot + ((k * kPer + i) * blockDim.x + threadIdx.x) * 16),
+                            reinterpret_cast<const char*>(t + c.at(k)) + 16 * i);
+    };
     auto fetch = [&](int64_t row, int st) {
         if constexpr (kRing) {
             if (row < r1) {
                 unsigned char* s = ring + st * stage;
+                const int64_t base = row * p.C;
                 if (dh) {
-                    fetch_row(s, x_out + row * p.C, c);
-                    fetch_row(s + off_h, dh + row * p.C, c);
+                    fetch_one(s, x_out + base);
+                    fetch_one(s + off_h, dh + base);
                 }
-                if (dx_out) fetch_row(s + off_d, dx_out + row * p.C, c);
-                if (y) fetch_row(s + off_y, y + row * p.C, c);
+                if (dx_out) fetch_one(s + off_d, dx_out + base);
+                if (y) fetch_one(s + off_y, y + base);
             }
             fetch_commit();
         }
     };
-    // kToken: dweight, dbias, dpost_weight sums of the CTA; else A, S, T of the current group
-    float sa[kCols] = {}, ss[kCols] = {}, st[kCols] = {};
-    bool flushed = false;
-    for (int i = 0; i < kBwdStages - 1; ++i) fetch(r0 + i, i);
-    int n = 0;
-    for (int64_t row = r0; row < r1; ++row, ++n) {
-        fetch(row + kBwdStages - 1, (n + kBwdStages - 1) % kBwdStages);
-        if constexpr (kRing) fetch_wait<kBwdStages - 1>();
-        const unsigned char* slot = ring + n % kBwdStages * stage;
-        float* rd = red[n & 1];
-        const int64_t base = row * p.C, grp = row / p.group_rows, gbase = grp * p.C;
-        auto get_x = [&](const TX* t, int off, float* v) {
-            if constexpr (kRing) slot_row<TX>(slot + off, c, v); else load_row<VEC>(t + base, c, v);
-        };
-        auto get_h = [&](const __nv_bfloat16* t, int off, float* v) {
-            if constexpr (kRing) slot_row<__nv_bfloat16>(slot + off, c, v); else load_row<VEC>(t + base, c, v);
-        };
-        // xh: x, centred, normalised; yh likewise
-        float xh[kCols], yh[kCols];
-        float rx = 1.f, ry = 1.f;
-        if (dh) get_x(x_out, 0, xh);
-        if (y) get_h(y, off_y, yh);
-        float mean[2] = {0.f, 0.f};
-        const bool lx = dh && p.norm == BSA_NORM_LAYER, ly = y && p.post == BSA_NORM_LAYER;
-        if (lx || ly) {
-            if (lx) mean[0] = sum_of(xh);
-            if (ly) mean[1] = sum_of(yh);
-            row_sum<false, 2>(mean, rd);
-            if (lx) centre(xh, mean[0] / p.c, c);
-            if (ly) centre(yh, mean[1] / p.c, c);
-        }
-        float d[kCols];                                  // total gradient of x_out
-        if (dx_out) {
-            get_x(dx_out, off_d, d);
-        } else {
+    // channels of one array of the row in ring stage `st` (or at `t`)
+    auto get = [&](const auto* t, int st, int off, float* v) {
+        constexpr int kPer = 8 * sizeof(*t) / 16;
 #pragma unroll
-            for (int i = 0; i < kCols; ++i) d[i] = 0.f;
-        }
-        float four[4] = {0.f, 0.f, 0.f, 0.f};            // sum xc^2, sum g, sum g xc, sum yc^2
-        float gr[kCols];
-        if (dh) {
-            get_h(dh, off_h, gr);
-            with_param(gr, p.weight, c, times);
-            if (p.scale) with_param(gr, p.scale + gbase, c, times1);
-            four[0] = square_of(xh);
-            four[1] = sum_of(gr);
+        for (int k = 0; k < R; ++k) {
+            if (!c.in(k)) {
 #pragma unroll
-            for (int i = 0; i < kCols; ++i) four[2] += gr[i] * xh[i];
-        }
-        if (y && p.post != BSA_NORM_NONE) four[3] = square_of(yh);
-        if (dh || (y && p.post != BSA_NORM_NONE)) row_sum<false, 4>(four, rd + 64);
-        if (dh) {
-            rx = rsqrtf(four[0] * p.inv_c + p.eps);
-            const float m0 = p.norm == BSA_NORM_LAYER ? four[1] * p.inv_c : 0.f, m1 = four[2] * rx * p.inv_c;
+                for (int e = 0; e < VEC; ++e) v[k * VEC + e] = 0.f;
+            } else if constexpr (kRing) {
+                const unsigned char* s = ring + st * stage + off + (k * kPer * blockDim.x + threadIdx.x) * 16;
+                if constexpr (sizeof(*t) == 2) {
+                    load_cols<8>(reinterpret_cast<const __nv_bfloat16*>(s), v + 8 * k);
+                } else {
 #pragma unroll
-            for (int i = 0; i < kCols; ++i) {
-                xh[i] *= rx;
-                d[i] += rx * (gr[i] - m0 - xh[i] * m1);
-            }
-            get_h(dh, off_h, gr);
-            if constexpr (kToken) {
-                if (g.dshift) store_row(g.dshift + gbase, c, gr);
-                if (g.dscale) {
-                    float t[kCols];
-#pragma unroll
-                    for (int i = 0; i < kCols; ++i) t[i] = xh[i];
-                    with_param(t, p.weight, c, times);
-                    with_param(t, p.bias, c, plus);
-#pragma unroll
-                    for (int i = 0; i < kCols; ++i) t[i] *= gr[i];
-                    store_row(g.dscale + gbase, c, t);
+                    for (int i = 0; i < 2; ++i) {
+                        const float4 f = *reinterpret_cast<const float4*>(s + i * blockDim.x * 16);
+                        v[8 * k + 4 * i] = f.x;
+                        v[8 * k + 4 * i + 1] = f.y;
+                        v[8 * k + 4 * i + 2] = f.z;
+                        v[8 * k + 4 * i + 3] = f.w;
+                    }
                 }
-                if (p.scale) with_param(gr, p.scale + gbase, c, times1);
+            } else {
+                load_cols<VEC>(t + c.at(k), v + k * VEC);
             }
+        }
+    };
+    auto each = [&](auto f) {
 #pragma unroll
-            for (int i = 0; i < kCols; ++i) {
-                sa[i] += gr[i] * xh[i];
-                ss[i] += gr[i];
+        for (int i = 0; i < NC; ++i) f(i);
+    };
+    auto param = [&](float* v, const float* q, auto f) {
+        if (!q) return;
+#pragma unroll
+        for (int k = 0; k < R; ++k)
+            if (c.in(k)) {
+                float t[VEC];
+                load_cols<VEC>(q + c.at(k), t);
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) v[k * VEC + e] = f(v[k * VEC + e], t[e]);
             }
+    };
+    auto store = [&](auto* t, const float* v) {
+#pragma unroll
+        for (int k = 0; k < R; ++k)
+            if (c.in(k)) store_cols<VEC>(t + c.at(k), v + k * VEC);
+    };
+    auto total = [&](const float* v) {
+        float s = 0.f;
+        each([&](int i) { s += v[i]; });
+        return s;
+    };
+
+    // kToken: dweight, dbias, dpost_weight sums of the CTA; else A, S, T of the current group
+    float sa[NC] = {}, ss[NC] = {}, st_[NC] = {};
+    float ca[NC], cg[NC];                                // weight (1 + scale), gate post_weight of the group
+    bool flushed = false;
+    int64_t left = 0, gbase = 0;                         // rows of the group still to come; its parameters
+    for (int i = 0; i < kBwdStages - 1; ++i) fetch(r0 + i, i);
+    // the first row's sums for its means; every later row's travel with the sums of the row before it
+    float sums[4 * G];
+    for (int i = 0; i < 4 * G; ++i) sums[i] = 0.f;
+    if (lx || ly) {
+        if constexpr (kRing) fetch_wait<kBwdStages - 2>();
+        float t[NC];
+        if (lx) {
+            get(x_out + r0 * p.C, 0, 0, t);
+            sums[3] = total(t);
+        }
+        if constexpr (kPost)
+            if (ly) {
+                get(y + r0 * p.C, 0, off_y, t);
+                sums[5] = total(t);
+            }
+        cta_sums<G>(sums, red[1]);
+    }
+    int st = 0;
+    for (int64_t row = r0; row < r1; ++row) {
+        const int nx = st + 1 == kBwdStages ? 0 : st + 1;            // the next row's stage
+        fetch(row + kBwdStages - 1, nx + 1 == kBwdStages ? 0 : nx + 1);
+        float* rd = red[(row - r0) & 1];
+        const int64_t base = row * p.C;
+        if (left == 0) {
+            const int64_t grp = row / p.group_rows;
+            left = (grp + 1) * p.group_rows - row;
+            gbase = grp * p.C;
+            each([&](int i) { ca[i] = cg[i] = 1.f; });
+            param(ca, p.weight, times);
+            if (p.scale) param(ca, p.scale + gbase, times1);
+            param(cg, p.post_weight, times);
+            if (p.gate) param(cg, p.gate + gbase, times);
+        }
+        --left;
+        const float mean_x = sums[3] / p.c, mean_y = kPost ? sums[4 * G - 3] / p.c : 0.f;
+        if constexpr (kRing) fetch_wait<kBwdStages - 2>();           // this row and the next
+        // xh: x centred, then normalised; yh likewise
+        float xh[NC], gh[NC], yh[NC], d[NC];
+        for (int i = 0; i < 4 * G; ++i) sums[i] = 0.f;               // sum xc^2, g, g xc, next x | yc^2, next y
+        if (dh) {
+            get(x_out + base, st, 0, xh);
+            get(dh + base, st, off_h, gh);
+            if (lx) {
+#pragma unroll
+                for (int k = 0; k < R; ++k)
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) xh[k * VEC + e] = c.in(k) ? xh[k * VEC + e] - mean_x : 0.f;
+            }
+            each([&](int i) {
+                const float gr = gh[i] * ca[i];
+                sums[0] += xh[i] * xh[i];
+                sums[1] += gr;
+                sums[2] += gr * xh[i];
+            });
+            if (lx && row + 1 < r1) {
+                get(x_out + base + p.C, nx, 0, d);
+                sums[3] = total(d);
+            }
+        }
+        if (y) get(y + base, st, off_y, yh);
+        if constexpr (kPost) {
+            if (ly) {
+#pragma unroll
+                for (int k = 0; k < R; ++k)
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) yh[k * VEC + e] = c.in(k) ? yh[k * VEC + e] - mean_y : 0.f;
+            }
+            each([&](int i) { sums[4] += yh[i] * yh[i]; });
+            if (ly && row + 1 < r1) {
+                get(y + base + p.C, nx, off_y, d);
+                sums[5] = total(d);
+            }
+        }
+        if (dx_out) {
+            get(dx_out + base, st, off_d, d);
+        } else {
+            each([&](int i) { d[i] = 0.f; });
+        }
+        if (dh || kPost) cta_sums<G>(sums, rd);
+        if (dh) {
+            const float rx = rsqrtf(sums[0] * p.inv_c + p.eps);
+            const float m0 = p.norm == BSA_NORM_LAYER ? sums[1] * p.inv_c : 0.f, m1 = sums[2] * rx * p.inv_c;
+            each([&](int i) {
+                xh[i] *= rx;
+                d[i] += rx * (gh[i] * ca[i] - m0 - xh[i] * m1);
+            });
+            if constexpr (kToken) {
+                if (g.dshift) store(g.dshift + gbase, gh);
+                if (g.dscale) {
+                    float t[NC];
+                    each([&](int i) { t[i] = xh[i]; });
+                    param(t, p.weight, times);
+                    param(t, p.bias, plus);
+                    each([&](int i) { t[i] *= gh[i]; });
+                    store(g.dscale + gbase, t);
+                }
+                if (p.scale) param(gh, p.scale + gbase, times1);
+            }
+            each([&](int i) {
+                sa[i] += gh[i] * xh[i];
+                ss[i] += gh[i];
+            });
         }
         if (y) {
-            if (p.post != BSA_NORM_NONE) {
-                ry = rsqrtf(four[3] * p.inv_c + p.eps);
-#pragma unroll
-                for (int i = 0; i < kCols; ++i) yh[i] *= ry;
+            float ry = 1.f;
+            if constexpr (kPost) {
+                ry = rsqrtf(sums[4] * p.inv_c + p.eps);
+                each([&](int i) { yh[i] *= ry; });
             }
-            float gy[kCols];
-#pragma unroll
-            for (int k = 0; k < kCols / VEC; ++k)
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) gy[k * VEC + e] = c.in(k) ? d[k * VEC + e] : 0.f;
             if constexpr (kToken) {
+                float t[NC];
                 if (g.dgate) {
-                    float t[kCols];
-#pragma unroll
-                    for (int i = 0; i < kCols; ++i) t[i] = yh[i];
-                    with_param(t, p.post_weight, c, times);
-#pragma unroll
-                    for (int i = 0; i < kCols; ++i) t[i] *= gy[i];
-                    store_row(g.dgate + gbase, c, t);
+                    each([&](int i) { t[i] = yh[i]; });
+                    param(t, p.post_weight, times);
+                    each([&](int i) { t[i] *= d[i]; });
+                    store(g.dgate + gbase, t);
                 }
-                if (p.gate) with_param(gy, p.gate + gbase, c, times);
-#pragma unroll
-                for (int i = 0; i < kCols; ++i) st[i] += gy[i] * yh[i];
+                each([&](int i) { t[i] = d[i]; });
+                if (p.gate) param(t, p.gate + gbase, times);
+                each([&](int i) { st_[i] += t[i] * yh[i]; });
             } else {
-#pragma unroll
-                for (int i = 0; i < kCols; ++i) st[i] += gy[i] * yh[i];
-                if (p.gate) with_param(gy, p.gate + gbase, c, times);
+                each([&](int i) { st_[i] += d[i] * yh[i]; });
             }
-            with_param(gy, p.post_weight, c, times);
-            if (p.post != BSA_NORM_NONE) {
-                float two[2] = {sum_of(gy), 0.f};
+            if constexpr (kPost) {
+                // channels past C: cg is 1 there, yh 0
+                float two[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int i = 0; i < kCols; ++i) two[1] += gy[i] * yh[i];
-                row_sum<false, 2>(two, rd + 192);
+                for (int k = 0; k < R; ++k)
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) {
+                        const float gy = c.in(k) ? d[k * VEC + e] * cg[k * VEC + e] : 0.f;
+                        two[0] += gy;
+                        two[1] += gy * yh[k * VEC + e];
+                    }
+                cta_sums<1>(two, rd + G * 4 * 32);
                 const float m0 = p.post == BSA_NORM_LAYER ? two[0] * p.inv_c : 0.f, m1 = two[1] * p.inv_c;
-#pragma unroll
-                for (int i = 0; i < kCols; ++i) gy[i] = ry * (gy[i] - m0 - yh[i] * m1);
+                each([&](int i) { yh[i] = ry * (d[i] * cg[i] - m0 - yh[i] * m1); });
+            } else {
+                each([&](int i) { yh[i] = d[i] * cg[i]; });
             }
-            store_row(dy + base, c, gy);
-#pragma unroll
-            for (int i = 0; i < kCols; ++i) d[i] *= p.res_scale;
+            store(dy + base, yh);
+            each([&](int i) { d[i] *= p.res_scale; });
         }
-        store_row(dx + base, c, d);
+        store(dx + base, d);
+        st = nx;
         if constexpr (!kToken) {
             // the group ends here, or this CTA's share of it does
-            const bool group_end = (row + 1) % p.group_rows == 0;
-            if (!group_end && row + 1 < r1) continue;
-            const bool whole = group_end && grp * p.group_rows >= r0;
-            const int piece = grp * p.group_rows < r0 ? 0 : 1;        // one that began earlier, or one that goes on
+            if (left > 0 && row + 1 < r1) continue;
+            const int64_t first = row + 1 + left - p.group_rows;      // the group's first row
+            const bool whole = left == 0 && first >= r0;
+            const int piece = first < r0 ? 0 : 1;                     // one that began earlier, or one that goes on
 #pragma unroll
-            for (int k = 0; k < kCols / VEC; ++k) {
+            for (int k = 0; k < R; ++k) {
                 if (!c.in(k)) continue;
 #pragma unroll
                 for (int e = 0; e < VEC; ++e) {
@@ -529,20 +660,20 @@ k_norm_bwd(const NormP p, const GradP g, const Ranges rg, const __nv_bfloat16* d
                     float* w = g.wsum + (int64_t)blockIdx.x * 3 * p.C + ch;
                     w[0] = (flushed ? w[0] : 0.f) + sc * sa[i];
                     w[p.C] = (flushed ? w[p.C] : 0.f) + sc * ss[i];
-                    w[2 * p.C] = (flushed ? w[2 * p.C] : 0.f) + gt * st[i];
+                    w[2 * p.C] = (flushed ? w[2 * p.C] : 0.f) + gt * st_[i];
                     if (whole) {
                         if (g.dscale)
                             g.dscale[gbase + ch] =
                                 (p.weight ? p.weight[ch] : 1.f) * sa[i] + (p.bias ? p.bias[ch] : 0.f) * ss[i];
                         if (g.dshift) g.dshift[gbase + ch] = ss[i];
-                        if (g.dgate) g.dgate[gbase + ch] = (p.post_weight ? p.post_weight[ch] : 1.f) * st[i];
+                        if (g.dgate) g.dgate[gbase + ch] = (p.post_weight ? p.post_weight[ch] : 1.f) * st_[i];
                     } else {
                         float* o = g.piece + ((int64_t)blockIdx.x * 2 + piece) * 3 * p.C + ch;
                         o[0] = sa[i];
                         o[p.C] = ss[i];
-                        o[2 * p.C] = st[i];
+                        o[2 * p.C] = st_[i];
                     }
-                    sa[i] = ss[i] = st[i] = 0.f;
+                    sa[i] = ss[i] = st_[i] = 0.f;
                 }
             }
             flushed = true;
@@ -551,13 +682,13 @@ k_norm_bwd(const NormP p, const GradP g, const Ranges rg, const __nv_bfloat16* d
     if constexpr (kToken) {
         float* w = g.wsum + (int64_t)blockIdx.x * 3 * p.C;
 #pragma unroll
-        for (int k = 0; k < kCols / VEC; ++k)
+        for (int k = 0; k < R; ++k)
             if (c.in(k))
 #pragma unroll
                 for (int e = 0; e < VEC; ++e) {
                     w[c.at(k) + e] = sa[k * VEC + e];
                     w[p.C + c.at(k) + e] = ss[k * VEC + e];
-                    w[2 * p.C + c.at(k) + e] = st[k * VEC + e];
+                    w[2 * p.C + c.at(k) + e] = st_[k * VEC + e];
                 }
     }
 }
@@ -642,13 +773,16 @@ int ctas_per_sm(int threads, int regs, int smem) {
 }
 
 // The gradient's CTAs (its workspace depends on them): as many as fit, 8 rows at least to each.
-constexpr int kBwdRegs = 168;
+constexpr int kRingBytes = 200 * 1024;
+int bwd_threads(int C) { return ((C + bwd_cols(C) - 1) / bwd_cols(C) + 31) / 32 * 32; }
+// bytes of a ring stage, 0: no ring (rows off the 16-byte grid, or too long)
 int bwd_stage_bytes(const bsa_norm_args& a) {
-    return a.C % 8 == 0 && row_threads(a.C) <= kRingThreads ? row_threads(a.C) * kCols * (2 * (a.dtype == BSA_BF16 ? 2 : 4) + 4) : 0;
+    const int bytes = bwd_threads(a.C) * bwd_cols(a.C) * (2 * (a.dtype == BSA_BF16 ? 2 : 4) + 4);
+    return a.C % 8 == 0 && bwd_cols(a.C) == 8 && kBwdStages * bytes <= kRingBytes ? bytes : 0;
 }
 int bwd_ctas(const bsa_plan& p, const bsa_norm_args& a) {
-    const int threads = row_threads(a.C);
-    const int per = ctas_per_sm(threads, threads <= kRingThreads ? kBwdRegs : 64, kBwdStages * bwd_stage_bytes(a));
+    const int threads = bwd_threads(a.C);
+    const int per = ctas_per_sm(threads, threads <= 512 ? 128 : threads <= 640 ? 96 : 64, kBwdStages * bwd_stage_bytes(a));
     return (int)std::min<int64_t>((int64_t)p.num_sms * per, ((int64_t)p.B * p.N + 7) / 8);
 }
 
@@ -676,23 +810,43 @@ cudaError_t fwd(const bsa_plan& p, const NormP& n, const void* x, const void* y,
     return cudaGetLastError();
 }
 
-template <typename TX, int VEC>
-cudaError_t bwd(const bsa_norm_args& a, const NormP& n, const GradP& g, const Ranges& rg, const void* dh,
-                const void* dx_out, const void* x_out, const void* y, void* dx, void* dy, cudaStream_t s) {
-    const int threads = row_threads(n.C);
-    const bool token = n.group_rows == 1;
-    auto kern = threads <= kRingThreads ? (token ? k_norm_bwd<TX, VEC, kRingThreads, true> : k_norm_bwd<TX, VEC, kRingThreads, false>)
-                               : (token ? k_norm_bwd<TX, VEC, 1024, true> : k_norm_bwd<TX, VEC, 1024, false>);
-    const int smem = kBwdStages * bwd_stage_bytes(a);
+struct BwdCall {
+    NormP n;
+    GradP g;
+    Ranges rg;
+    const void *dh, *dx_out, *x_out, *y;
+    void *dx, *dy;
+    int threads, stage;
+    cudaStream_t s;
+};
+
+template <typename TX, int VEC, int NC, int kThreads, bool kToken, bool kPost, bool kRing>
+cudaError_t bwd_t(const BwdCall& b) {
+    auto kern = k_norm_bwd<TX, VEC, NC, kThreads, kToken, kPost, kRing>;
+    const int smem = kRing ? kBwdStages * b.stage : 0;
     if (smem > 48 * 1024)
         if (cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) return e;
-    kern<<<rg.n, threads, smem, s>>>(n, g, rg, (const __nv_bfloat16*)dh, (const TX*)dx_out, (const TX*)x_out,
-                                     (const __nv_bfloat16*)y, (TX*)dx, (__nv_bfloat16*)dy);
-    if (cudaError_t e = cudaGetLastError()) return e;
-    const int64_t groups = token ? 0 : n.rows / n.group_rows;
-    k_norm_bwd_join<<<dim3((n.C + 31) / 32, 1 + (unsigned)std::min<int64_t>(groups, 1024)), dim3(32, kShares), 0, s>>>(
-        n, g, rg, groups);
+    kern<<<b.rg.n, b.threads, smem, b.s>>>(b.n, b.g, b.rg, (const __nv_bfloat16*)b.dh, (const TX*)b.dx_out,
+                                           (const TX*)b.x_out, (const __nv_bfloat16*)b.y, (TX*)b.dx, (__nv_bfloat16*)b.dy);
     return cudaGetLastError();
+}
+template <typename TX, int VEC, int NC, int kThreads, bool kRing>
+cudaError_t bwd_opts(const BwdCall& b) {
+    const bool token = b.n.group_rows == 1, post = b.y && b.n.post != BSA_NORM_NONE;
+    if (token) return post ? bwd_t<TX, VEC, NC, kThreads, true, true, kRing>(b) : bwd_t<TX, VEC, NC, kThreads, true, false, kRing>(b);
+    return post ? bwd_t<TX, VEC, NC, kThreads, false, true, kRing>(b) : bwd_t<TX, VEC, NC, kThreads, false, false, kRing>(b);
+}
+template <typename TX>
+cudaError_t bwd(const BwdCall& b) {
+    if (b.n.C % 8 == 0 && b.stage > 0) {
+        if (b.threads <= 512) return bwd_opts<TX, 8, 8, 512, true>(b);
+        if (b.threads <= 640) return bwd_opts<TX, 8, 8, 640, true>(b);
+        return bwd_opts<TX, 8, 8, 1024, true>(b);
+    }
+    if (bwd_cols(b.n.C) == 16)
+        return b.n.C % 8 == 0 ? bwd_opts<TX, 8, 16, 1024, false>(b) : bwd_opts<TX, 1, 16, 1024, false>(b);
+    if (b.n.C % 8 == 0) return bwd_opts<TX, 8, 8, 1024, false>(b);
+    return b.threads <= 512 ? bwd_opts<TX, 1, 8, 512, false>(b) : bwd_opts<TX, 1, 8, 1024, false>(b);
 }
 
 }  // namespace
@@ -720,12 +874,13 @@ cudaError_t launch_norm_bwd(const bsa_plan& p, const bsa_norm_args& a, const Nor
     g.dweight = out.dweight; g.dbias = out.dbias; g.dpost = out.dpost_weight;
     g.piece = (float*)ws;
     g.wsum = g.piece + (size_t)rg.n * 6 * a.C;
-    const bool wide = a.C % 8 == 0;
-    if (a.dtype == BSA_BF16)
-        return wide ? bwd<__nv_bfloat16, 8>(a, n, g, rg, dh, dx_out, x_out, y, dx, dy, s)
-                    : bwd<__nv_bfloat16, 1>(a, n, g, rg, dh, dx_out, x_out, y, dx, dy, s);
-    return wide ? bwd<float, 8>(a, n, g, rg, dh, dx_out, x_out, y, dx, dy, s)
-                : bwd<float, 1>(a, n, g, rg, dh, dx_out, x_out, y, dx, dy, s);
+    const BwdCall b{n, g, rg, dh, dx_out, x_out, y, dx, dy, bwd_threads(a.C), bwd_stage_bytes(a), s};
+    cudaError_t e = a.dtype == BSA_BF16 ? bwd<__nv_bfloat16>(b) : bwd<float>(b);
+    if (e != cudaSuccess) return e;
+    const int64_t groups = n.group_rows == 1 ? 0 : n.rows / n.group_rows;
+    k_norm_bwd_join<<<dim3((n.C + 31) / 32, 1 + (unsigned)std::min<int64_t>(groups, 1024)), dim3(32, kShares), 0, s>>>(
+        n, g, rg, groups);
+    return cudaGetLastError();
 }
 
 }  // namespace bsa
