@@ -57,6 +57,7 @@ _P = ctypes.c_void_p
 _I = ctypes.c_int
 _I64 = ctypes.c_int64
 _SZ = ctypes.c_size_t
+_I64x9 = _I64 * 9
 
 
 class NormArgs(ctypes.Structure):
@@ -579,9 +580,14 @@ def sparse_attn_fp8v(plan: Plan, q, k, v, row_ptr, col_idx, workspace=None, out=
 # that a launch still uses is handed out again.
 
 class _On:
-    """Makes `stream` (None: the current one) the current stream of the plan's device, and that device current."""
+    """Makes `stream` (None: the current one) the current stream of the plan's device, and that device current;
+    entered, it is the raw stream."""
 
     def __init__(self, plan, stream):
+        self._dev = self._stream = None
+        self._index = plan.device.index
+        if stream is None and torch.cuda.current_device() == plan.device.index:
+            return                                                    # nothing to change
         if stream is not None and not isinstance(stream, torch.cuda.Stream):
             raw = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
             stream = torch.cuda.ExternalStream(raw, device=plan.device)
@@ -590,24 +596,29 @@ class _On:
         self._dev, self._stream = torch.cuda.device(plan.device), torch.cuda.stream(stream)
 
     def __enter__(self):
-        self._dev.__enter__()
-        self._stream.__enter__()
-        return torch.cuda.current_stream().cuda_stream
+        if self._dev is not None:
+            self._dev.__enter__()
+            self._stream.__enter__()
+            return torch.cuda.current_stream().cuda_stream
+        return torch._C._cuda_getCurrentRawStream(self._index)        # a tenth of current_stream()'s time
 
     def __exit__(self, *exc):
-        self._stream.__exit__(*exc)
-        self._dev.__exit__(*exc)
+        if self._dev is not None:
+            self._stream.__exit__(*exc)
+            self._dev.__exit__(*exc)
 
 
 def _need(plan, t, name, dtypes, shape, dense=True):
+    if isinstance(t, torch.Tensor) and t.device == plan.device and t.dtype in dtypes and t.shape == shape and (
+            not dense or t.is_contiguous()):
+        return
     if not isinstance(t, torch.Tensor) or t.device != plan.device:
         raise ValueError(f"{name} must be a tensor on {plan.device}")
     if t.dtype not in dtypes:
         raise ValueError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, not {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {list(shape)}, not {list(t.shape)}")
-    if dense and not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+    raise ValueError(f"{name} must be contiguous")
 
 
 def _workspace(plan, need, workspace):
@@ -617,7 +628,7 @@ def _workspace(plan, need, workspace):
     return workspace
 
 
-_BF16 = (torch.bfloat16,)
+_BF16, _F32, _STREAM = (torch.bfloat16,), (torch.float32,), (torch.bfloat16, torch.float32)
 
 
 def _cross_inputs(plan, q, k, v, kv_len, key_mask):
@@ -635,7 +646,7 @@ def _cross_inputs(plan, q, k, v, kv_len, key_mask):
         _need(plan, kv_len, "kv_len", (torch.int32,), (plan.B,))
     if key_mask is not None:
         _need(plan, key_mask, "key_mask", (torch.bool, torch.uint8), (plan.B, M))
-    return M, Hkv, (_I64 * 9)(*(t.stride(i) for t in (q, k, v) for i in range(3)))
+    return M, Hkv, _I64x9(*q.stride()[:3], *k.stride()[:3], *v.stride()[:3])
 
 
 def cross_attn(plan: Plan, q, k, v, kv_len=None, key_mask=None, return_lse=False, workspace=None, out=None,
@@ -649,7 +660,7 @@ def cross_attn(plan: Plan, q, k, v, kv_len=None, key_mask=None, return_lse=False
     if out is not None:
         _need(plan, out, "out", _BF16, q.shape)
     with _On(plan, stream) as s:
-        o = torch.empty(q.shape, dtype=q.dtype, device=plan.device) if out is None else out
+        o = torch.empty_like(q, memory_format=torch.contiguous_format) if out is None else out
         lse = torch.empty(plan.B, plan.H, plan.N, dtype=torch.float32, device=plan.device) if return_lse else None
         ws = _workspace(plan, _lib.bsa_cross_attn_workspace_size(plan.handle, M, Hkv, 0), workspace)
         _check(_lib.bsa_cross_attn(plan.handle, _ptr(q), _ptr(k), _ptr(v), M, Hkv, strides, _ptr(kv_len),
@@ -663,11 +674,11 @@ def cross_attn_backward(plan: Plan, do, q, k, v, o, lse, kv_len=None, key_mask=N
     M, Hkv, strides = _cross_inputs(plan, q, k, v, kv_len, key_mask)
     _need(plan, do, "do", _BF16, q.shape)
     _need(plan, o, "o", _BF16, q.shape)
-    _need(plan, lse, "lse", (torch.float32,), (plan.B, plan.H, plan.N))
+    _need(plan, lse, "lse", _F32, (plan.B, plan.H, plan.N))
     with _On(plan, stream) as s:
-        dq = torch.empty(q.shape, dtype=q.dtype, device=plan.device)
-        dk = torch.empty(k.shape, dtype=k.dtype, device=plan.device)
-        dv = torch.empty(v.shape, dtype=v.dtype, device=plan.device)
+        dq = torch.empty_like(q, memory_format=torch.contiguous_format)
+        dk = torch.empty_like(k, memory_format=torch.contiguous_format)
+        dv = torch.empty_like(v, memory_format=torch.contiguous_format)
         ws = _workspace(plan, _lib.bsa_cross_attn_workspace_size(plan.handle, M, Hkv, 1), workspace)
         _check(_lib.bsa_cross_attn_bwd(plan.handle, _ptr(q), _ptr(k), _ptr(v), M, Hkv, strides, _ptr(kv_len),
                                        _ptr(key_mask), _ptr(o), _ptr(lse), _ptr(do), _ptr(dq), _ptr(dk), _ptr(dv),
@@ -680,22 +691,20 @@ def _norm_inputs(plan, x, gate, scale, shift, weight, bias, post_weight, norm, p
     if not isinstance(x, torch.Tensor) or x.dim() != 3:
         raise ValueError("x must be [B, N, C]")
     C = x.shape[2]
-    _need(plan, x, "x", (torch.bfloat16, torch.float32), (plan.B, plan.N, C))
+    _need(plan, x, "x", _STREAM, (plan.B, plan.N, C))
+    first = gate if gate is not None else scale if scale is not None else shift
     groups = 1
-    for t, name in ((gate, "gate"), (scale, "scale"), (shift, "shift")):
-        if t is None:
-            continue
-        if not isinstance(t, torch.Tensor) or t.dim() != 3:
-            raise ValueError(f"{name} must be [B, groups, C]")
-        if groups != 1 and t.shape[1] != groups:
-            raise ValueError("gate, scale and shift must have the same number of groups")
-        groups = t.shape[1]
-    for t, name in ((gate, "gate"), (scale, "scale"), (shift, "shift")):
-        if t is not None:
-            _need(plan, t, name, (torch.float32,), (plan.B, groups, C))
+    if first is not None:
+        if not isinstance(first, torch.Tensor) or first.dim() != 3:
+            raise ValueError("gate, scale and shift must be [B, groups, C]")
+        groups = first.shape[1]
+        shape = (plan.B, groups, C)
+        for t, name in ((gate, "gate"), (scale, "scale"), (shift, "shift")):
+            if t is not None:
+                _need(plan, t, name, _F32, shape)
     for t, name in ((weight, "weight"), (bias, "bias"), (post_weight, "post_weight")):
         if t is not None:
-            _need(plan, t, name, (torch.float32,), (C,))
+            _need(plan, t, name, _F32, (C,))
     return NormArgs(C, groups, BSA_BF16 if x.dtype == torch.bfloat16 else BSA_F32, norm, post_norm, eps, res_scale,
                     _ptr(gate), _ptr(scale), _ptr(shift), _ptr(weight), _ptr(bias), _ptr(post_weight))
 
@@ -708,7 +717,7 @@ def norm_modulate(plan: Plan, x, scale=None, shift=None, weight=None, bias=None,
     if out is not None:
         _need(plan, out, "out", _BF16, x.shape)
     with _On(plan, stream) as s:
-        h = torch.empty(x.shape, dtype=torch.bfloat16, device=plan.device) if out is None else out
+        h = torch.empty_like(x, dtype=torch.bfloat16) if out is None else out
         _check(_lib.bsa_norm_modulate(plan.handle, ctypes.byref(a), _ptr(x), _ptr(h), s), "bsa_norm_modulate")
     return h
 
