@@ -28,7 +28,7 @@ namespace {
 using namespace tc;
 using namespace cross;
 
-constexpr int kRowWarp = 8, kMmaWarp = 12;
+constexpr int kRowWarp = 8, kMmaWarp = 12, kPollWarp = 13;
 constexpr int kThreads = 16 * 32;
 constexpr uint32_t kTmemCols = 512;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -83,8 +83,8 @@ __device__ __forceinline__ void end_cta(uint32_t tmem) {
 }
 
 // ------------------------------------------------------------------ query side
-// warps 0-7 softmax, 8-11 rows (D, then dQ to memory), 12 MMA, 13 K ring,
-// 14 V ring, 15 Q and dO.  Q and dO go to TMEM (tcgen05.cp), so that S and dP
+// warps 0-7 softmax, 8-11 rows (D, then dQ to memory), 12 MMA, 13 polls for it,
+// 14 K ring, 15 V ring with Q and dO.  Q and dO go to TMEM (tcgen05.cp), so that S and dP
 // read only K and V from shared memory.
 struct DqP {
     Keys keys;
@@ -177,21 +177,13 @@ k_cross_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
 
     if (warp == kMmaWarp) {
         constexpr uint32_t idesc_s = instr_desc(kKeys, 0), idesc_dq = instr_desc(D, 1);
-        uint32_t ua = 0, uc = 0, items_a = 0, items_c = 0;        // steps and items: scores made, dQ added
-        DqWalk cur, ahead;
+        uint32_t ua = 0, uc = 0;                                  // steps: scores made, dQ added
+        DqWalk cur, ahead;                                        // ahead: the step whose scores are made next
         cur.seek(prm);
         ahead = cur;
-        // everything the scores of `ahead` read is there
-        auto ready = [&] {
-            const uint32_t st = ua % L::kStages, ph = (ua / L::kStages) & 1;
-            if (!warp_wait<kEvery>(bar(K_FULL + st), ph, ctl) || !warp_wait<kEvery>(bar(V_FULL + st), ph, ctl)) return false;
-            if (ahead.t > 0) return true;
-            // the item's Q and dO to TMEM, once the item before it has made its last scores
-            if (items_a > 0 && !warp_wait<kEvery>(bar(AB_FREE), (items_a - 1) & 1, ctl)) return false;
-            if (!warp_wait<kEvery>(bar(QD_FULL), items_a & 1, ctl)) return false;
-            ++items_a;
-            fence_after();
-            if (elect_one()) {
+        auto scores = [&] {                                       // one lane
+            const uint32_t st = ua % L::kStages, buf = (ua & 1) * kKeys;
+            if (ahead.t == 0) {                                   // the item's Q and dO to TMEM
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk) {
                     const uint32_t off = (kk / 4) * L::kSlabQ + (kk % 4) * 32;
@@ -200,11 +192,6 @@ k_cross_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
                 }
                 commit(bar(QD_EMPTY));
             }
-            __syncwarp();
-            return true;
-        };
-        auto scores = [&] {                                       // one lane
-            const uint32_t st = ua % L::kStages, buf = (ua & 1) * kKeys;
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk)
                 mma_ts(tmem + L::colS + buf, tmem + L::colQ + kk * 8,
@@ -219,18 +206,14 @@ k_cross_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
             commit(bar(V_EMPTY + st));
             if (ahead.last()) commit(bar(AB_FREE));
         };
-        for (int i = 0; i < 2 && ahead.ok && (ok = ready()); ++i) {
+        for (int i = 0; i < 2 && ahead.ok && (ok = meet(true)); ++i) {
             fence_after();
             if (elect_one()) scores();
             __syncwarp();
             ++ua;
             ahead.next(prm);
         }
-        for (; cur.ok && ok; cur.next(prm), ++uc) {
-            if (ahead.ok && !(ok = ready())) break;
-            // dQ of the item before this one has been read
-            if (cur.t == 0 && items_c++ > 0 && !(ok = warp_wait<kEvery>(bar(DQ_FREE), items_c & 1, ctl))) break;
-            if (!(ok = warp_wait<kEvery>(bar(DS_FULL + (uc & 1)), (uc >> 1) & 1, ctl))) break;
+        for (; cur.ok && ok && (ok = meet(true)); cur.next(prm), ++uc) {
             fence_after();
             if (elect_one()) {
                 const uint32_t st = uc % L::kStages;
@@ -249,13 +232,40 @@ k_cross_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
                 ahead.next(prm);
             }
         }
-        if (!ok && lane == 0) { ctl->abort = 1; record_error(prm.err, BSA_EDEVICE, -3); }
         if (elect_one()) {
             commit(bar(DRAIN));
             mbar_drain(bar(DRAIN), 0);
         }
         __syncwarp();
-    } else if (warp == kMmaWarp + 1) {
+    } else if (warp == kPollWarp) {
+        // what each of the MMA warp's steps waits for
+        uint32_t ua = 0, uc = 0, items_a = 0, items_c = 0;
+        DqWalk cur, ahead;
+        cur.seek(prm);
+        ahead = cur;
+        auto scores_ready = [&] {
+            const uint32_t st = ua % L::kStages, ph = (ua / L::kStages) & 1;
+            ++ua;
+            if (!warp_wait<kEvery>(bar(K_FULL + st), ph, ctl) || !warp_wait<kEvery>(bar(V_FULL + st), ph, ctl)) return false;
+            if (ahead.t > 0) return true;
+            // Q and dO have landed, and the item before has made its last scores (a copy into TMEM is not ordered
+            // behind the products that read the same columns)
+            if (items_a > 0 && !warp_wait<kEvery>(bar(AB_FREE), (items_a - 1) & 1, ctl)) return false;
+            return warp_wait<kEvery>(bar(QD_FULL), items_a++ & 1, ctl);
+        };
+        for (int i = 0; i < 2 && ahead.ok && ok; ++i) {
+            ok = meet(scores_ready());
+            ahead.next(prm);
+        }
+        for (; cur.ok && ok; cur.next(prm), ++uc) {
+            bool go = !ahead.ok || scores_ready();
+            // dQ of the item before this one has been read
+            if (go && cur.t == 0 && items_c++ > 0) go = warp_wait<kEvery>(bar(DQ_FREE), items_c & 1, ctl);
+            ok = meet(go && warp_wait<kEvery>(bar(DS_FULL + (uc & 1)), (uc >> 1) & 1, ctl));
+            if (ahead.ok) ahead.next(prm);
+        }
+        if (!ok && lane == 0) { ctl->abort = 1; record_error(prm.err, BSA_EDEVICE, -3); }
+    } else if (warp == kPollWarp + 1) {
         // K ring.  dQ += dS K: rows of states that do not count become zeros (0 * NaN is NaN)
         uint32_t u = 0, raw = 0;
         DqWalk w;
@@ -290,11 +300,23 @@ k_cross_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
         if (!ok && lane == 0) { ctl->abort = 1; record_error(prm.err, BSA_EDEVICE, -1); }
         for (uint32_t st = 0; st < L::kStages; ++st)
             if (u > st) mbar_drain(bar(K_FULL + st), ((u - 1 - st) / L::kStages) & 1);
-    } else if (warp == kMmaWarp + 2) {
+    } else if (warp == kPollWarp + 2) {
+        // V ring, and each item's Q and dO ahead of its first V tile
         if (lane == 0) {
-            uint32_t u = 0;
+            uint32_t u = 0, n = 0;
             DqWalk w;
             for (w.seek(prm); w.ok; w.next(prm), ++u) {
+                if (w.t == 0) {
+                    if (n > 0 && !(ok = mbar_sleep<kEvery>(bar(QD_EMPTY), (n - 1) & 1, ctl))) break;
+                    ++n;
+                    mbar_expect_tx(bar(QD_FULL), 2 * L::kQBytes);
+                    for (int s = 0; s < D / 64; ++s) {
+                        tma_load_4d(sbase + L::offQ + s * L::kSlabQ, &tmQ, s * 64, w.it.tile * kTile, w.it.h, w.it.b,
+                                    bar(QD_FULL));
+                        tma_load_4d(sbase + L::offQ + L::kQBytes + s * L::kSlabQ, &tmDO, s * 64, w.it.tile * kTile, w.it.h,
+                                    w.it.b, bar(QD_FULL));
+                    }
+                }
                 const int st = u % L::kStages;
                 if (u >= L::kStages && !(ok = mbar_sleep<kEvery>(bar(V_EMPTY + st), (u / L::kStages - 1) & 1, ctl))) break;
                 mbar_expect_tx(bar(V_FULL + st), L::kTileBytes);
@@ -305,21 +327,6 @@ k_cross_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
             if (!ok) { ctl->abort = 1; record_error(prm.err, BSA_EDEVICE, -2); }
             for (uint32_t st = 0; st < L::kStages; ++st)
                 if (u > st) mbar_drain(bar(V_FULL + st), ((u - 1 - st) / L::kStages) & 1);
-        }
-    } else if (warp == kMmaWarp + 3) {
-        if (lane == 0) {
-            uint32_t n = 0;
-            DqWalk w;
-            for (w.seek(prm); w.ok; w.next_item(prm), ++n) {
-                if (n > 0 && !(ok = mbar_sleep<kEvery>(bar(QD_EMPTY), (n - 1) & 1, ctl))) break;
-                mbar_expect_tx(bar(QD_FULL), 2 * L::kQBytes);
-                for (int s = 0; s < D / 64; ++s) {
-                    tma_load_4d(sbase + L::offQ + s * L::kSlabQ, &tmQ, s * 64, w.it.tile * kTile, w.it.h, w.it.b, bar(QD_FULL));
-                    tma_load_4d(sbase + L::offQ + L::kQBytes + s * L::kSlabQ, &tmDO, s * 64, w.it.tile * kTile, w.it.h,
-                                w.it.b, bar(QD_FULL));
-                }
-            }
-            if (!ok) { ctl->abort = 1; record_error(prm.err, BSA_EDEVICE, -6); }
             if (n > 0) mbar_drain(bar(QD_FULL), (n - 1) & 1);
         }
     } else if (warp < kRowWarp) {
@@ -472,8 +479,8 @@ k_cross_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
 }
 
 // -------------------------------------------------------------------- key side
-// warps 0-7 softmax, 8-11 dK and dV to memory, 12 MMA, 13 Q / dO ring with the
-// rows' lse and D, 14 K and V.  An item: a key tile of one key head and a share
+// warps 0-7 softmax, 8-11 dK and dV to memory, 12 MMA, 13 polls for it, 14 Q /
+// dO ring with the rows' lse and D, 15 K and V.  An item: a key tile of one key head and a share
 // of the (query head, 64-token) steps that read it.
 struct DkvP {
     Keys keys;
@@ -565,14 +572,10 @@ k_cross_dkv(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUt
 
     if (warp == kMmaWarp) {
         constexpr uint32_t idesc_s = instr_desc(kKeys, 0), idesc_g = instr_desc(D, 1);
-        uint32_t ua = 0, uc = 0, items_a = 0, items_c = 0;
+        uint32_t ua = 0, uc = 0;
         DkvWalk cur, ahead;
         cur.seek(prm);
         ahead = cur;
-        auto ready = [&] {
-            if (!warp_wait<kEvery>(bar(ST_FULL + ua % L::kStages), (ua / L::kStages) & 1, ctl)) return false;
-            return !ahead.first() || warp_wait<kEvery>(bar(KV_FULL), items_a++ & 1, ctl);
-        };
         auto scores = [&] {                                       // one lane
             const uint32_t buf = (ua & 1) * kKeys, q = sbase + L::offQ + ua % L::kStages * 2 * L::kTileBytes;
 #pragma unroll
@@ -587,17 +590,14 @@ k_cross_dkv(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUt
             commit(bar(S_FULL + (ua & 1)));
             if (ahead.last()) commit(bar(KV_EMPTY));
         };
-        for (int i = 0; i < 2 && ahead.ok && (ok = ready()); ++i) {
+        for (int i = 0; i < 2 && ahead.ok && (ok = meet(true)); ++i) {
             fence_after();
             if (elect_one()) scores();
             __syncwarp();
             ++ua;
             ahead.next(prm);
         }
-        for (; cur.ok && ok; cur.next(prm), ++uc) {
-            if (ahead.ok && !(ok = ready())) break;
-            if (cur.first() && items_c++ > 0 && !(ok = warp_wait<kEvery>(bar(ACC_FREE), items_c & 1, ctl))) break;
-            if (!(ok = warp_wait<kEvery>(bar(PD_FULL + (uc & 1)), (uc >> 1) & 1, ctl))) break;
+        for (; cur.ok && ok && (ok = meet(true)); cur.next(prm), ++uc) {
             fence_after();
             if (elect_one()) {
                 const uint32_t st = uc % L::kStages, q = sbase + L::offQ + st * 2 * L::kTileBytes, buf = (uc & 1) * kKeys;
@@ -619,13 +619,35 @@ k_cross_dkv(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUt
                 ahead.next(prm);
             }
         }
-        if (!ok && lane == 0) { ctl->abort = 1; record_error(prm.err, BSA_EDEVICE, -3); }
         if (elect_one()) {
             commit(bar(DRAIN));
             mbar_drain(bar(DRAIN), 0);
         }
         __syncwarp();
-    } else if (warp == kMmaWarp + 1) {
+    } else if (warp == kPollWarp) {
+        uint32_t ua = 0, uc = 0, items_a = 0, items_c = 0;
+        DkvWalk cur, ahead;
+        cur.seek(prm);
+        ahead = cur;
+        auto scores_ready = [&] {
+            const uint32_t st = ua % L::kStages, ph = (ua / L::kStages) & 1;
+            ++ua;
+            return warp_wait<kEvery>(bar(ST_FULL + st), ph, ctl) &&
+                   (!ahead.first() || warp_wait<kEvery>(bar(KV_FULL), items_a++ & 1, ctl));
+        };
+        for (int i = 0; i < 2 && ahead.ok && ok; ++i) {
+            ok = meet(scores_ready());
+            ahead.next(prm);
+        }
+        for (; cur.ok && ok; cur.next(prm), ++uc) {
+            bool go = !ahead.ok || scores_ready();
+            // dK and dV of the item before this one have been read
+            if (go && cur.first() && items_c++ > 0) go = warp_wait<kEvery>(bar(ACC_FREE), items_c & 1, ctl);
+            ok = meet(go && warp_wait<kEvery>(bar(PD_FULL + (uc & 1)), (uc >> 1) & 1, ctl));
+            if (ahead.ok) ahead.next(prm);
+        }
+        if (!ok && lane == 0) { ctl->abort = 1; record_error(prm.err, BSA_EDEVICE, -3); }
+    } else if (warp == kPollWarp + 1) {
         uint32_t u = 0;
         DkvWalk w;
         for (w.seek(prm); w.ok; w.next(prm), ++u) {
@@ -659,7 +681,7 @@ k_cross_dkv(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUt
         if (!ok && lane == 0) { ctl->abort = 1; record_error(prm.err, BSA_EDEVICE, -1); }
         for (uint32_t st = 0; st < L::kStages; ++st)
             if (u > st) mbar_drain(bar(ST_FULL + st), ((u - 1 - st) / L::kStages) & 1);
-    } else if (warp == kMmaWarp + 2) {
+    } else if (warp == kPollWarp + 2) {
         if (lane == 0) {
             uint32_t n = 0;
             DkvWalk w;

@@ -51,6 +51,22 @@ __device__ __forceinline__ bool elect_one() {
     return p != 0;
 }
 
+// A meeting of two warps (named barrier 1) that tells both whether both are well.  The MMA warp learns this way from
+// a polling warp that its operands are ready: a warp that has issued MMAs stalls on its next shared-memory access
+// until the tensor cores have taken them, and a mbarrier probe is one; the named barrier is not.
+__device__ __forceinline__ bool meet(bool ok) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %1, 0;\n\t"
+        "bar.red.and.pred q, 1, 64, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"((uint32_t)ok)
+        : "memory");
+    return r != 0;
+}
+
 // A bounded wait that lets the hardware suspend the thread between probes: for the roles that wait most of the
 // time (loads, output), whose spinning would take issue slots from the softmax warps.
 template <uint32_t kEvery>
