@@ -83,12 +83,12 @@ __device__ __forceinline__ void end_cta(uint32_t tmem) {
 }
 
 // ------------------------------------------------------------------ query side
-// warps 0-7 softmax, 8-11 rows (D, then dQ to memory), 12 MMA, 13 polls for it,
-// 14 K ring, 15 V ring with Q and dO.  Q and dO go to TMEM (tcgen05.cp), so that S and dP
+// warps 0-7 softmax, 8-11 rows (the next item's Q, dO and D, then dQ to
+// memory), 12 MMA, 13 polls for it, 14 K ring, 15 V ring.  Q and dO go to TMEM (tcgen05.cp), so that S and dP
 // read only K and V from shared memory.
 struct DqP {
     Keys keys;
-    const __nv_bfloat16* o;
+    const __nv_bfloat16 *o, *d_o;
     const float* lse;
     float* dsum;
     int32_t* err;
@@ -167,7 +167,6 @@ k_cross_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
     float* row_vals = reinterpret_cast<float*>(smem + L::offRows);
     const uint32_t tmem = begin_cta<kBars>(bar(0), ctl, reinterpret_cast<uint32_t*>(smem + L::offMisc + 16), prm.wait_ns,
                                            [](int i) -> uint32_t {
-                                               if (i == QD_EMPTY) return 5;                       // copies, 4 row warps
                                                if (i == ROWS_EMPTY || i == ROWS_EMPTY + 1) return 8;
                                                if ((i >= DS_FULL && i < ROWS_EMPTY) || i == DQ_FREE) return 4;
                                                return 1;
@@ -301,22 +300,10 @@ k_cross_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
         for (uint32_t st = 0; st < L::kStages; ++st)
             if (u > st) mbar_drain(bar(K_FULL + st), ((u - 1 - st) / L::kStages) & 1);
     } else if (warp == kPollWarp + 2) {
-        // V ring, and each item's Q and dO ahead of its first V tile
         if (lane == 0) {
-            uint32_t u = 0, n = 0;
+            uint32_t u = 0;
             DqWalk w;
             for (w.seek(prm); w.ok; w.next(prm), ++u) {
-                if (w.t == 0) {
-                    if (n > 0 && !(ok = mbar_sleep<kEvery>(bar(QD_EMPTY), (n - 1) & 1, ctl))) break;
-                    ++n;
-                    mbar_expect_tx(bar(QD_FULL), 2 * L::kQBytes);
-                    for (int s = 0; s < D / 64; ++s) {
-                        tma_load_4d(sbase + L::offQ + s * L::kSlabQ, &tmQ, s * 64, w.it.tile * kTile, w.it.h, w.it.b,
-                                    bar(QD_FULL));
-                        tma_load_4d(sbase + L::offQ + L::kQBytes + s * L::kSlabQ, &tmDO, s * 64, w.it.tile * kTile, w.it.h,
-                                    w.it.b, bar(QD_FULL));
-                    }
-                }
                 const int st = u % L::kStages;
                 if (u >= L::kStages && !(ok = mbar_sleep<kEvery>(bar(V_EMPTY + st), (u / L::kStages - 1) & 1, ctl))) break;
                 mbar_expect_tx(bar(V_FULL + st), L::kTileBytes);
@@ -327,7 +314,6 @@ k_cross_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
             if (!ok) { ctl->abort = 1; record_error(prm.err, BSA_EDEVICE, -2); }
             for (uint32_t st = 0; st < L::kStages; ++st)
                 if (u > st) mbar_drain(bar(V_FULL + st), ((u - 1 - st) / L::kStages) & 1);
-            if (n > 0) mbar_drain(bar(QD_FULL), (n - 1) & 1);
         }
     } else if (warp < kRowWarp) {
         // ------------------------------------------------------------------ softmax
@@ -349,30 +335,36 @@ k_cross_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
                 const bool all = prm.keys.bits(it.b, it.len, t * kKeys, lane, bits);
                 if (!(ok = warp_wait<kEvery>(bar(S_FULL + g), (u >> 1) & 1, ctl))) break;
                 fence_after();
+                // 16 columns at a time, the next ones on their way from TMEM
+                uint32_t sv[2][16], dv[2][16];
+                tmem_ld16(ts, sv[0]);
+                tmem_ld16(tp, dv[0]);
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    uint32_t sv[32], dv[32], pk[16];
-                    tmem_ld32(ts + c * 32, sv);
-                    tmem_ld32(tp + c * 32, dv);
+                for (int c = 0; c < 4; ++c) {
                     tmem_wait_ld();
+                    if (c < 3) {
+                        tmem_ld16(ts + (c + 1) * 16, sv[(c + 1) & 1]);
+                        tmem_ld16(tp + (c + 1) * 16, dv[(c + 1) & 1]);
+                    }
+                    const uint32_t *x = sv[c & 1], *dp = dv[c & 1];
+                    uint32_t pk[8];
 #pragma unroll
-                    for (int e = 0; e < 32; e += 2) {
+                    for (int e = 0; e < 16; e += 2) {
                         float x0, x1, d0, d1;
-                        ffma2(x0, x1, __uint_as_float(sv[e]), __uint_as_float(sv[e + 1]), prm.scale_log2, prm.scale_log2,
+                        ffma2(x0, x1, __uint_as_float(x[e]), __uint_as_float(x[e + 1]), prm.scale_log2, prm.scale_log2,
                               neg_lse, neg_lse);
-                        fadd2(d0, d1, __uint_as_float(dv[e]), __uint_as_float(dv[e + 1]), neg_d, neg_d);
+                        fadd2(d0, d1, __uint_as_float(dp[e]), __uint_as_float(dp[e + 1]), neg_d, neg_d);
                         const float p0 = ex2_mufu(x0), p1 = ex2_mufu(x1);
                         fmul2(d0, d1, d0, d1, p0, p1);
                         pk[e / 2] = pack_bf16(d0, d1);
                     }
                     if (!all) {
+                        const uint32_t on = bits[c / 2] >> (16 * (c & 1));
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) {
-                            const uint32_t on = bits[c] >> (2 * e);
-                            pk[e] &= (on & 1 ? 0xffffu : 0u) | (on & 2 ? 0xffff0000u : 0u);
-                        }
+                        for (int e = 0; e < 8; ++e)
+                            pk[e] &= (on >> (2 * e) & 1 ? 0xffffu : 0u) | (on >> (2 * e + 1) & 1 ? 0xffff0000u : 0u);
                     }
-                    tmem_st16(ts + c * 16, pk);
+                    tmem_st8(ts + c * 8, pk);
                 }
                 tmem_wait_st();
                 fence_before();
@@ -388,18 +380,59 @@ k_cross_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
         const int quad = warp & 3, r = 32 * quad + lane;
         const uint32_t tq = tmem + ((uint32_t)(32 * quad) << 16) + L::colDQ;
         unsigned char* stage = smem + L::offOut + quad * 4096;
-        const unsigned char* sdo = smem + L::offQ + L::kQBytes;
-        uint32_t nr = 0, nd = 0;
+        uint32_t nr = 0, nd = 0, nl = 0;
+        // Q and dO of an item, once the copies of the one before have read theirs
+        auto load = [&](const DqItem& it) {
+            if (warp != kRowWarp) return true;
+            if (nl > 0 && !warp_sleep<kEvery>(bar(QD_EMPTY), (nl - 1) & 1, ctl)) return false;
+            ++nl;
+            if (lane == 0) {
+                mbar_expect_tx(bar(QD_FULL), 2 * L::kQBytes);
+                for (int s = 0; s < D / 64; ++s) {
+                    tma_load_4d(sbase + L::offQ + s * L::kSlabQ, &tmQ, s * 64, it.tile * kTile, it.h, it.b, bar(QD_FULL));
+                    tma_load_4d(sbase + L::offQ + L::kQBytes + s * L::kSlabQ, &tmDO, s * 64, it.tile * kTile, it.h, it.b,
+                                bar(QD_FULL));
+                }
+            }
+            __syncwarp();
+            return true;
+        };
         auto rows = [&](const DqItem& it) {
-            if (!warp_sleep<kEvery>(bar(QD_FULL), nr & 1, ctl)) return false;
             if (nr >= 2 && !warp_sleep<kEvery>(bar(ROWS_EMPTY + (nr & 1)), ((nr >> 1) - 1) & 1, ctl)) return false;
-            const int n = it.tile * kTile + r;
-            float d = 0.f, lse2 = 0.f;
+            // D of the warp's 32 rows: D / 8 lanes to a row, 16 bytes of O and dO a lane
+            constexpr int kLanes = D / 8, kPer = 32 / kLanes;
+            const int sub = lane / kLanes, c = lane % kLanes, n0 = it.tile * kTile + 32 * quad;
+            const int64_t at = (((int64_t)it.b * prm.N + n0) * prm.H + it.h) * D + c * 8;
+            float t[kLanes];                                          // this lane's part of row i * kPer + sub
+#pragma unroll
+            for (int i0 = 0; i0 < kLanes; i0 += 4) {
+                uint4 ov[4], gv[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int rr = (i0 + i) * kPer + sub;
+                    const int64_t e = at + (int64_t)rr * prm.H * D;
+                    const bool in = n0 + rr < prm.N;
+                    ov[i] = in ? __ldg(reinterpret_cast<const uint4*>(prm.o + e)) : make_uint4(0, 0, 0, 0);
+                    gv[i] = in ? __ldg(reinterpret_cast<const uint4*>(prm.d_o + e)) : make_uint4(0, 0, 0, 0);
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) t[i0 + i] = dot8(ov[i], gv[i]);
+            }
+            // sums over a row's lanes, half as many values carried after each step (shuffles share the path that the
+            // products' operands saturate: 80 of them took 8000 cycles here); lane c ends with i = c
+#pragma unroll
+            for (int x = kLanes / 2; x > 0; x >>= 1) {
+                const bool up = c & x;
+#pragma unroll
+                for (int i = 0; i < x; ++i) {
+                    const float keep = up ? t[i + x] : t[i], give = up ? t[i] : t[i + x];
+                    t[i] = keep + __shfl_xor_sync(0xffffffffu, give, x);
+                }
+            }
+            const float d = __shfl_sync(0xffffffffu, t[0], (lane % kPer) * kLanes + lane / kPer);
+            float lse2 = 0.f;
+            const int n = n0 + lane;
             if (n < prm.N) {
-                const uint4* orow = reinterpret_cast<const uint4*>(prm.o + (((int64_t)it.b * prm.N + n) * prm.H + it.h) * D);
-#pragma unroll 4
-                for (int c = 0; c < D / 8; ++c)
-                    d += dot8(__ldg(orow + c), *reinterpret_cast<const uint4*>(sdo + swizzled(r, c, L::kSlabQ)));
                 const int64_t i = ((int64_t)it.b * prm.H + it.h) * prm.N + n;
                 const float l = prm.lse[i];
                 lse2 = l == -INFINITY ? 0.f : l * kLog2e;             // no valid state: every key is masked
@@ -409,24 +442,21 @@ k_cross_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
             rv[0] = lse2;
             rv[kTile] = d;
             __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(bar(ROWS_FULL + (nr & 1)));
-                mbar_arrive(bar(QD_EMPTY));
-            }
+            if (lane == 0) mbar_arrive(bar(ROWS_FULL + (nr & 1)));
             ++nr;
             return true;
         };
         DqWalk pre;
         pre.seek(prm);
         if (pre.ok) {
-            ok = rows(pre.it);
+            ok = load(pre.it) && rows(pre.it);
             pre.next_item(prm);
         }
         DqItem it;
         for (int k = 0; ok && item_at(prm, k, it); ++k) {
             if (it.nt > 0) {
                 if (pre.ok) {                                         // the next item's D before this one's dQ
-                    if (!(ok = rows(pre.it))) break;
+                    if (!(ok = load(pre.it) && rows(pre.it))) break;
                     pre.next_item(prm);
                 }
                 if (!(ok = warp_sleep<kEvery>(bar(DQ_DONE), nd & 1, ctl))) break;
@@ -434,35 +464,34 @@ k_cross_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
                 fence_after();
             }
             const int row0 = it.tile * kTile + 32 * quad;
+            uint32_t pk[D / 2];                                       // the row in bf16
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+                uint32_t v[32];
+                if (it.nt > 0) {
+                    tmem_ld32(tq + c * 32, v);
+                    tmem_wait_ld();
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) v[e] = 0u;
+                }
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                    pk[16 * c + e] = pack_bf16(__uint_as_float(v[2 * e]) * prm.scale, __uint_as_float(v[2 * e + 1]) * prm.scale);
+            }
+            if (it.nt > 0) {                                          // dQ may take the next item
+                fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(DQ_FREE));
+            }
 #pragma unroll
             for (int s = 0; s < D / 64; ++s) {
                 if (lane == 0) bulk_wait_read();
                 __syncwarp();
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    uint32_t v[32];
-                    if (it.nt > 0) {
-                        tmem_ld32(tq + s * 64 + c * 32, v);
-                        tmem_wait_ld();
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) v[e] = 0u;
-                    }
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        uint4 w;
-                        w.x = pack_bf16(__uint_as_float(v[8 * e + 0]) * prm.scale, __uint_as_float(v[8 * e + 1]) * prm.scale);
-                        w.y = pack_bf16(__uint_as_float(v[8 * e + 2]) * prm.scale, __uint_as_float(v[8 * e + 3]) * prm.scale);
-                        w.z = pack_bf16(__uint_as_float(v[8 * e + 4]) * prm.scale, __uint_as_float(v[8 * e + 5]) * prm.scale);
-                        w.w = pack_bf16(__uint_as_float(v[8 * e + 6]) * prm.scale, __uint_as_float(v[8 * e + 7]) * prm.scale);
-                        *reinterpret_cast<uint4*>(stage + swizzled(lane, 4 * c + e, 0)) = w;
-                    }
-                }
-                if (it.nt > 0 && s == D / 64 - 1) {
-                    fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(bar(DQ_FREE));
-                }
+                for (int c = 0; c < 8; ++c)
+                    *reinterpret_cast<uint4*>(stage + swizzled(lane, c, 0)) =
+                        make_uint4(pk[32 * s + 4 * c], pk[32 * s + 4 * c + 1], pk[32 * s + 4 * c + 2], pk[32 * s + 4 * c + 3]);
                 fence_proxy_async();
                 __syncwarp();
                 if (lane == 0 && row0 < prm.N) {
@@ -472,6 +501,7 @@ k_cross_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
             }
         }
         if (!ok) { ctl->abort = 1; record_error(prm.err, BSA_EDEVICE, -5); }
+        if (nl > 0) mbar_drain(bar(QD_FULL), (nl - 1) & 1);           // what this warp loaded has landed
         tmem_wait_ld();
         if (lane == 0) bulk_wait();
     }
@@ -665,8 +695,8 @@ k_cross_dkv(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUt
             float* rv = row_vals + st * 2 * kKeys + lane;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                rv[32 * i] = l[i] == -INFINITY ? INFINITY : l[i];
-                rv[kKeys + 32 * i] = d[i];
+                rv[32 * i] = l[i] == -INFINITY ? -INFINITY : -l[i];   // negated: addends
+                rv[kKeys + 32 * i] = -d[i];
             }
             __syncwarp();
             if (lane == 0) {
@@ -714,23 +744,29 @@ k_cross_dkv(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUt
                 if (!(ok = warp_wait<kEvery>(bar(S_FULL + g), (u >> 1) & 1, ctl))) break;
                 fence_after();
                 const float* rv = row_vals + st * 2 * kKeys;
+                uint32_t sv[2][16], dv[2][16];
+                tmem_ld16(ts, sv[0]);
+                tmem_ld16(tp, dv[0]);
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    uint32_t sv[32], dv[32], pk[16], dk[16];
-                    tmem_ld32(ts + c * 32, sv);
-                    tmem_ld32(tp + c * 32, dv);
+                for (int c = 0; c < 4; ++c) {
                     tmem_wait_ld();
+                    if (c < 3) {
+                        tmem_ld16(ts + (c + 1) * 16, sv[(c + 1) & 1]);
+                        tmem_ld16(tp + (c + 1) * 16, dv[(c + 1) & 1]);
+                    }
+                    const uint32_t *x = sv[c & 1], *dp = dv[c & 1];
+                    uint32_t pk[8], dk[8];
 #pragma unroll
-                    for (int e = 0; e < 32; e += 4) {
-                        const float4 l4 = *reinterpret_cast<const float4*>(rv + c * 32 + e);
-                        const float4 d4 = *reinterpret_cast<const float4*>(rv + kKeys + c * 32 + e);
+                    for (int e = 0; e < 16; e += 4) {
+                        const float4 l4 = *reinterpret_cast<const float4*>(rv + c * 16 + e);
+                        const float4 d4 = *reinterpret_cast<const float4*>(rv + kKeys + c * 16 + e);
                         const float l[4] = {l4.x, l4.y, l4.z, l4.w}, d[4] = {d4.x, d4.y, d4.z, d4.w};
 #pragma unroll
                         for (int f = 0; f < 4; f += 2) {
                             float x0, x1, d0, d1;
-                            ffma2(x0, x1, __uint_as_float(sv[e + f]), __uint_as_float(sv[e + f + 1]), prm.scale_log2,
-                                  prm.scale_log2, -l[f], -l[f + 1]);
-                            fadd2(d0, d1, __uint_as_float(dv[e + f]), __uint_as_float(dv[e + f + 1]), -d[f], -d[f + 1]);
+                            ffma2(x0, x1, __uint_as_float(x[e + f]), __uint_as_float(x[e + f + 1]), prm.scale_log2,
+                                  prm.scale_log2, l[f], l[f + 1]);
+                            fadd2(d0, d1, __uint_as_float(dp[e + f]), __uint_as_float(dp[e + f + 1]), d[f], d[f + 1]);
                             const float p0 = ex2_mufu(x0), p1 = ex2_mufu(x1);
                             fmul2(d0, d1, d0, d1, p0, p1);
                             pk[(e + f) / 2] = pack_bf16(p0, p1);
@@ -739,10 +775,10 @@ k_cross_dkv(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUt
                     }
                     if (!on) {
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) pk[e] = dk[e] = 0u;
+                        for (int e = 0; e < 8; ++e) pk[e] = dk[e] = 0u;
                     }
-                    tmem_st16(ts + c * 16, pk);
-                    tmem_st16(tp + c * 16, dk);
+                    tmem_st8(ts + c * 8, pk);
+                    tmem_st8(tp + c * 8, dk);
                 }
                 tmem_wait_st();
                 fence_before();
@@ -908,6 +944,7 @@ cudaError_t launch_cross_bwd_tc(const bsa_plan& p, const CrossArgs& a, const voi
     DqP pq;
     pq.keys = Keys{a.kv_len, a.key_mask, (int)a.M};
     pq.o = (const __nv_bfloat16*)o;
+    pq.d_o = (const __nv_bfloat16*)d_o;
     pq.lse = lse;
     pq.dsum = (float*)ws;
     pq.err = p.d_err;
