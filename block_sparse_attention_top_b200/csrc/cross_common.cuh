@@ -13,6 +13,28 @@ namespace cross {
 constexpr int kTile = 128;           // query rows of a tensor-core tile
 constexpr int kKeys = 64;            // keys of one
 
+// n / d by a multiplication, n < 2^31: the walks over work items divide in every role, and a division's code in each
+// place adds up (these kernels are sensitive to code size: 16 warps in seven roles share the instruction caches, and
+// at 94 KB of code instruction fetches took most of the time).
+struct Div {
+    uint32_t d, m, s;
+    Div() = default;
+    explicit Div(int64_t by) : d((uint32_t)by), m(0), s(0) {
+        if (d > 1) {
+            while ((1ull << s) < d) ++s;
+            m = (uint32_t)(((1ull << (31 + s)) + d - 1) / d);
+            --s;
+        }
+    }
+    __device__ __forceinline__ uint32_t quot(uint32_t n) const { return m ? __umulhi(n, m) >> s : n; }
+    // quotient, and n becomes the remainder
+    __device__ __forceinline__ uint32_t split(uint32_t& n) const {
+        const uint32_t q = quot(n);
+        n -= q * d;
+        return q;
+    }
+};
+
 // Valid states of batch entry b.
 struct Keys {
     const int32_t* kv_len;           // [B] or null
@@ -40,6 +62,17 @@ struct Keys {
     }
 };
 
+// Zeros in the rows of a K or V tile in shared memory whose state does not count (D / 8 lanes to a row).
+template <int D>
+__device__ __forceinline__ void zero_rows(unsigned char* tile, const uint32_t* bits, int lane) {
+    constexpr int kLanes = D / 8, kPer = 32 / kLanes;
+    const int c = lane % kLanes;
+#pragma unroll 1
+    for (int i = lane / kLanes; i < kKeys; i += kPer)
+        if (!((i < 32 ? bits[0] : bits[1]) >> (i % 32) & 1))
+            *reinterpret_cast<uint4*>(tile + (c / 8) * kKeys * 128 + i * 128 + (c % 8) * 16) = make_uint4(0, 0, 0, 0);
+}
+
 // One lane of a converged warp (the same one every time).
 __device__ __forceinline__ bool elect_one() {
     uint32_t p;
@@ -64,6 +97,9 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* r) {
                  ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
                  : "memory");
 }
+
+// A descriptor `bytes` further on (a multiple of 16, inside the shared memory window).
+__device__ __forceinline__ uint64_t desc_at(uint64_t desc, uint32_t bytes) { return desc + (bytes >> 4); }
 
 // A meeting of two warps (named barrier 1) that tells both whether both are well.  The MMA warp learns this way from
 // a polling warp that its operands are ready: a warp that has issued MMAs stalls on its next shared-memory access

@@ -58,7 +58,8 @@ struct FwdP {
     Keys keys;
     float* lse;
     int32_t* err;
-    int N, H, G, tiles, per_item, units, items;   // units: items of one head
+    int N, H, tiles, per_item, items;
+    Div units, heads, G;             // items of one head; query heads; query heads of a key head
     float scale_log2;
     unsigned long long wait_ns;
 };
@@ -70,10 +71,11 @@ struct Item {
 __device__ __forceinline__ bool item_at(const FwdP& p, int k, Item& it) {
     const int idx = k * gridDim.x + blockIdx.x;
     if (idx >= p.items) return false;
-    const int bh = idx / p.units;
-    it.b = bh / p.H;
-    it.h = bh % p.H;
-    it.tile = (idx - bh * p.units) * p.per_item;
+    uint32_t rest = (uint32_t)idx;
+    uint32_t bh = p.units.split(rest);
+    it.tile = (int)rest * p.per_item;
+    it.b = (int)p.heads.split(bh);
+    it.h = (int)bh;
     it.ng = min(p.per_item, p.tiles - it.tile);
     it.len = p.keys.count(it.b);
     it.nt = (it.len + kKeys - 1) / kKeys;
@@ -83,17 +85,17 @@ __device__ __forceinline__ bool item_at(const FwdP& p, int k, Item& it) {
 // The key tiles of this CTA's items, in the order every role walks them.
 struct Walk {
     Item it;
-    int k = 0, t = 0;
-    bool ok;
-    __device__ __forceinline__ void seek(const FwdP& p) {
-        while ((ok = item_at(p, k, it)) && it.nt == 0) ++k;
-    }
-    __device__ __forceinline__ void open(const FwdP& p) { seek(p); }
-    __device__ __forceinline__ void next(const FwdP& p) {
-        if (++t < it.nt) return;
+    int k = -1, t = 0;
+    bool ok = true;
+    __device__ __forceinline__ Walk() { it.nt = 0; }
+    __device__ __forceinline__ bool next(const FwdP& p) {
+        if (++t < it.nt) return true;
         t = 0;
-        ++k;
-        seek(p);
+        do {
+            ++k;
+            ok = item_at(p, k, it);
+        } while (ok && it.nt == 0);
+        return ok;
     }
 };
 
@@ -116,13 +118,12 @@ __device__ __forceinline__ void ex2_fma2(float x0, float x1, float& y0, float& y
 constexpr int kFmaPairs = 2;         // pairs of every 8 that take the FMA pipe
 
 // 32 scores to 32 probabilities (16 bf16 pairs); adds them to acc.
-template <bool kMixed>
 __device__ __forceinline__ void exp_chunk(const uint32_t* x, float scale, float neg_m, float* acc, uint32_t* pk) {
 #pragma unroll
     for (int c = 0; c < 32; c += 2) {
         float x0, x1, p0, p1;
         ffma2(x0, x1, __uint_as_float(x[c]), __uint_as_float(x[c + 1]), scale, scale, neg_m, neg_m);
-        if (kMixed && (c / 2) % 8 >= 8 - kFmaPairs) {
+        if ((c / 2) % 8 >= 8 - kFmaPairs) {
             ex2_fma2(x0, x1, p0, p1);
         } else {
             p0 = ex2_mufu(x0);
@@ -134,7 +135,8 @@ __device__ __forceinline__ void exp_chunk(const uint32_t* x, float scale, float 
     }
 }
 
-// -inf where a state does not count
+// -inf where a state does not count.  (On the FMA pipe such a score gives 2^-126, not 0: nothing beside a row's sum,
+// and its row of V is zero.)
 __device__ __forceinline__ void mask_cols(uint32_t* s, uint32_t bits) {
 #pragma unroll
     for (int c = 0; c < 32; ++c)
@@ -190,13 +192,13 @@ k_cross_fwd(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUt
             uint32_t u = 0, nq[2] = {0, 0};
             bool ok = true;
             Walk w;
-            for (w.open(prm); w.ok && ok; w.next(prm), ++u) {
+            for (; w.next(prm); ++u) {
                 const int st = u % L::kStages;
                 if (u >= L::kStages && !(ok = mbar_sleep<kEvery>(bar(K_EMPTY + st), (u / L::kStages - 1) & 1, ctl))) break;
                 mbar_expect_tx(bar(K_FULL + st), L::kTileBytes);
                 for (int s = 0; s < D / 64; ++s)
                     tma_load_4d(sbase + L::offK + st * L::kTileBytes + s * L::kSlab, &tmK, s * 64, w.t * kKeys,
-                                w.it.h / prm.G, w.it.b, bar(K_FULL + st));
+                                (int)prm.G.quot(w.it.h), w.it.b, bar(K_FULL + st));
                 if (w.t == 0)
                     for (int g = 0; g < w.it.ng && ok; ++g) {
                         if (nq[g] > 0 && !(ok = mbar_sleep<kEvery>(bar(Q_EMPTY + g), (nq[g] - 1) & 1, ctl))) break;
@@ -209,12 +211,10 @@ k_cross_fwd(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUt
                 if (!ok) { ++u; break; }
                 // The next item's Q, on its way to L2 while this item runs: a slab behind every K tile but the first
                 // few, since a later load waits for the copies issued before it.
-                if (w.t >= 2 && w.t < 2 + 2 * (D / 64)) {
-                    Walk n = w;
-                    ++n.k;
-                    n.seek(prm);
+                Item n;
+                if (w.t >= 2 && w.t < 2 + 2 * (D / 64) && item_at(prm, w.k + 1, n)) {
                     const int g = (w.t - 2) / (D / 64), s = (w.t - 2) % (D / 64);
-                    if (n.ok && g < n.it.ng) prefetch_4d(&tmQ, s * 64, (n.it.tile + g) * kTile, n.it.h, n.it.b);
+                    if (g < n.ng) prefetch_4d(&tmQ, s * 64, (n.tile + g) * kTile, n.h, n.b);
                 }
             }
             if (!ok) { ctl->abort = 1; record_error(prm.err, BSA_EDEVICE, -1); }
@@ -229,7 +229,7 @@ k_cross_fwd(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUt
         uint32_t u = 0, raw = 0;
         bool ok = true;
         Walk w;
-        for (w.open(prm); w.ok; w.next(prm), ++u) {
+        for (; w.next(prm); ++u) {
             const int st = u % L::kStages;
             if (u >= L::kStages && !(ok = warp_sleep<kEvery>(bar(V_EMPTY + st), (u / L::kStages - 1) & 1, ctl))) break;
             uint32_t bits[2];
@@ -241,7 +241,7 @@ k_cross_fwd(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUt
             if (lane == 0) {
                 mbar_expect_tx(full, L::kTileBytes);
                 for (int s = 0; s < D / 64; ++s)
-                    tma_load_4d(dst + s * L::kSlab, &tmV, s * 64, w.t * kKeys, w.it.h / prm.G, w.it.b, full);
+                    tma_load_4d(dst + s * L::kSlab, &tmV, s * 64, w.t * kKeys, (int)prm.G.quot(w.it.h), w.it.b, full);
             }
             if (fix) {
                 const bool landed = warp_wait<kEvery>(full, raw & 1, ctl);
@@ -251,10 +251,7 @@ k_cross_fwd(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUt
                     break;
                 }
                 ++raw;
-                for (int i = 0; i < kKeys; ++i)                  // a row of a slab: 8 lanes of 16 bytes
-                    if (!(bits[i / 32] >> (i % 32) & 1) && lane < D / 8)
-                        *reinterpret_cast<uint4*>(smem + (dst - sbase) + (lane / 8) * L::kSlab + i * 128 +
-                                                  (lane % 8) * 16) = make_uint4(0, 0, 0, 0);
+                zero_rows<D>(smem + (dst - sbase), bits, lane);
                 fence_proxy_async();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(V_FULL + st));
@@ -277,64 +274,59 @@ k_cross_fwd(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUt
             return warp_wait<kEvery>(bar(K_FULL + uk % L::kStages), (uk / L::kStages) & 1, ctl) &&
                    (w.t > 0 || g >= w.it.ng || warp_wait<kEvery>(bar(Q_FULL + g), nq++ & 1, ctl));
         };
-        // S[sk & 1] = Q_g K^T; a step without this query tile only passes the stage on (one lane)
-        auto qk = [&](const Walk& w) {
-            const int st = uk % L::kStages;
-            if (g < w.it.ng) {
-#pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk)
-                    mma_ss(ts + (sk & 1) * kKeys, smem_desc(q_tile + (kk / 4) * L::kSlabQ + (kk % 4) * 32, 16, 1024),
-                           smem_desc(sbase + L::offK + st * L::kTileBytes + (kk / 4) * L::kSlab + (kk % 4) * 32, 16, 1024),
-                           idesc_qk, kk > 0);
-                commit(bar(S_FULL + 2 * g + (sk & 1)));
-                commit(bar(K_EMPTY + st));
-                if (w.t == w.it.nt - 1) commit(bar(Q_EMPTY + g));
-            } else {
-                mbar_arrive(bar(K_EMPTY + st));
-            }
-        };
+        const uint64_t dq = smem_desc(q_tile, 16, 1024), dk = smem_desc(sbase + L::offK, 16, 1024),
+                       dv = smem_desc(sbase + L::offV, L::kSlab, 1024);
         Walk cur, ahead;                                 // ahead: the step whose scores are made next
-        cur.open(prm);
-        ahead = cur;
-        for (int i = 0; i < 2 && ahead.ok && (ok = qk_ready(ahead)); ++i) {
-            fence_after();
-            if (elect_one()) qk(ahead);
-            __syncwarp();
-            ++uk;
-            sk += g < ahead.it.ng;
-            ahead.next(prm);
-        }
-        for (; cur.ok && ok; cur.next(prm), ++uv) {
-            const int st = uv % L::kStages;
-            // everything but P first: a warp that polls behind its own MMAs waits until the tensor cores have taken them
-            if (!(ok = warp_wait<kEvery>(bar(V_FULL + st), (uv / L::kStages) & 1, ctl))) break;
-            if (ahead.ok && !(ok = qk_ready(ahead))) break;
-            if (g < cur.it.ng) {
+        cur.next(prm);
+        ahead.next(prm);
+        for (int made = 0; made > 0 || ahead.ok;) {      // scores made and not yet used
+            const bool pv = made == 2 || !ahead.ok, more = ahead.ok;
+            const int sv = uv % L::kStages, sq = uk % L::kStages;
+            const bool pv_g = pv && g < cur.it.ng, qk_g = more && g < ahead.it.ng;
+            // everything but P first
+            if (more && !(ok = qk_ready(ahead))) break;
+            if (pv && !(ok = warp_wait<kEvery>(bar(V_FULL + sv), (uv / L::kStages) & 1, ctl))) break;
+            if (pv_g) {
                 // the item before this one has been read out of O_g
                 if (cur.t == 0 && no++ > 0 && !(ok = warp_wait<kEvery>(bar(O_FREE + g), no & 1, ctl))) break;
                 if (!(ok = warp_wait<kEvery>(bar(P_FULL + 2 * g + (sp & 1)), (sp >> 1) & 1, ctl))) break;
             }
             fence_after();
             if (elect_one()) {
-                if (g < cur.it.ng) {
+                if (pv_g) {
 #pragma unroll
                     for (int kk = 0; kk < kKeys / 16; ++kk)
-                        mma_ts(to, ts + (sp & 1) * kKeys + kk * 8,
-                               smem_desc(sbase + L::offV + st * L::kTileBytes + kk * 16 * 128, L::kSlab, 1024), idesc_pv,
+                        mma_ts(to, ts + (sp & 1) * kKeys + kk * 8, desc_at(dv, sv * L::kTileBytes + kk * 16 * 128), idesc_pv,
                                cur.t > 0 || kk > 0);
                     commit(bar(PV_DONE + g));
-                    commit(bar(V_EMPTY + st));
+                    commit(bar(V_EMPTY + sv));
                     if (cur.t == cur.it.nt - 1) commit(bar(O_DONE + g));
-                } else {
-                    mbar_arrive(bar(V_EMPTY + st));
+                } else if (pv) {
+                    mbar_arrive(bar(V_EMPTY + sv));
                 }
-                if (ahead.ok) qk(ahead);
+                if (qk_g) {                              // S[sk & 1] = Q_g K^T
+#pragma unroll
+                    for (int kk = 0; kk < D / 16; ++kk)
+                        mma_ss(ts + (sk & 1) * kKeys, desc_at(dq, (kk / 4) * L::kSlabQ + (kk % 4) * 32),
+                               desc_at(dk, sq * L::kTileBytes + (kk / 4) * L::kSlab + (kk % 4) * 32), idesc_qk, kk > 0);
+                    commit(bar(S_FULL + 2 * g + (sk & 1)));
+                    commit(bar(K_EMPTY + sq));
+                    if (ahead.t == ahead.it.nt - 1) commit(bar(Q_EMPTY + g));
+                } else if (more) {                       // a step without this query tile passes the stage on
+                    mbar_arrive(bar(K_EMPTY + sq));
+                }
             }
             __syncwarp();
-            sp += g < cur.it.ng;
-            if (ahead.ok) {
+            if (pv) {
+                sp += pv_g;
+                ++uv;
+                --made;
+                cur.next(prm);
+            }
+            if (more) {
+                sk += qk_g;
                 ++uk;
-                sk += g < ahead.it.ng;
+                ++made;
                 ahead.next(prm);
             }
         }
@@ -377,17 +369,10 @@ k_cross_fwd(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUt
                 const float neg_m = m == -INFINITY ? 0.f : -m;        // no valid state so far
                 float acc[4] = {};
                 uint32_t pk[kKeys / 2];
-                if (all) {
-                    exp_chunk<true>(sv, prm.scale_log2, neg_m, acc, pk);
-                    tmem_st16(tsb, pk);
-                    exp_chunk<true>(sv + 32, prm.scale_log2, neg_m, acc, pk + 16);
-                    tmem_st16(tsb + 16, pk + 16);
-                } else {
-                    exp_chunk<false>(sv, prm.scale_log2, neg_m, acc, pk);
-                    tmem_st16(tsb, pk);
-                    exp_chunk<false>(sv + 32, prm.scale_log2, neg_m, acc, pk + 16);
-                    tmem_st16(tsb + 16, pk + 16);
-                }
+                exp_chunk(sv, prm.scale_log2, neg_m, acc, pk);
+                tmem_st16(tsb, pk);
+                exp_chunk(sv + 32, prm.scale_log2, neg_m, acc, pk + 16);
+                tmem_st16(tsb + 16, pk + 16);
                 l = l * alpha + ((acc[0] + acc[1]) + (acc[2] + acc[3]));
                 if (__any_sync(0xffffffffu, grow)) {
                     // PV(t-1) is the tile before this one; PV(t-2) was complete before S(t) was, so the parity is exact
@@ -428,7 +413,7 @@ k_cross_fwd(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUt
         for (int k = 0; ok && item_at(prm, k, it); ++k)
             for (int g = 0; g < it.ng; ++g) {
                 const int row0 = (it.tile + g) * kTile + 32 * quad, n = row0 + lane;
-                float l = 0.f, m = 0.f;
+                float l = 0.f, m = -INFINITY;
                 if (it.nt > 0) {
                     // the last PV is complete, so its P and with it l and m were written before
                     if (!(ok = warp_sleep<kEvery>(bar(O_DONE + g), done[g] & 1, ctl))) break;
@@ -438,11 +423,12 @@ k_cross_fwd(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUt
                     m = slot[kTile];
                     ++done[g];
                 }
-                const float inv = l == 0.f ? 0.f : 1.f / l;           // zeros for a row without a valid state
+                const bool empty = m == -INFINITY;                    // no valid state: zeros
+                const float inv = empty ? 0.f : 1.f / l;
                 if (prm.lse && n < prm.N)
                     prm.lse[((int64_t)it.b * prm.H + it.h) * prm.N + n] =
-                        l == 0.f ? -INFINITY : 0.69314718055994531f * (m + log2f(l));
-#pragma unroll
+                        empty ? -INFINITY : 0.69314718055994531f * (m + log2f(l));
+#pragma unroll 1
                 for (int s = 0; s < D / 64; ++s) {
                     uint32_t o[64];
                     if (it.nt > 0) {
@@ -520,12 +506,14 @@ cudaError_t launch_cross_fwd_tc(const bsa_plan& p, const CrossArgs& a, void* o, 
     prm.err = p.d_err;
     prm.N = (int)p.N;
     prm.H = p.H;
-    prm.G = p.H / a.Hkv;
+    prm.heads = Div(p.H);
+    prm.G = Div(p.H / a.Hkv);
     prm.tiles = (int)((p.N + kTile - 1) / kTile);
     // two tiles to an item unless that leaves SMs without one
     prm.per_item = (int64_t)p.B * p.H * ((prm.tiles + 1) / 2) >= p.num_sms ? 2 : 1;
-    prm.units = (prm.tiles + prm.per_item - 1) / prm.per_item;
-    prm.items = p.B * p.H * prm.units;
+    const int units = (prm.tiles + prm.per_item - 1) / prm.per_item;
+    prm.units = Div(units);
+    prm.items = p.B * p.H * units;
     prm.scale_log2 = 1.4426950408889634f / sqrtf((float)p.d);
     prm.wait_ns = p.wait_ns;
     return p.d == 128 ? launch_d<128>(p, a, prm, o, s) : launch_d<64>(p, a, prm, o, s);
