@@ -92,7 +92,8 @@ struct DqP {
     const float* lse;
     float* dsum;
     int32_t* err;
-    int N, H, G, tiles, items;
+    int N, H, items;
+    Div tiles, heads, G;             // query tiles of a head; query heads; query heads of a key head
     float scale, scale_log2;
     unsigned long long wait_ns;
 };
@@ -119,29 +120,30 @@ struct DqItem {
 __device__ __forceinline__ bool item_at(const DqP& p, int k, DqItem& it) {
     const int idx = k * gridDim.x + blockIdx.x;
     if (idx >= p.items) return false;
-    const int bh = idx / p.tiles;
-    it.b = bh / p.H;
-    it.h = bh % p.H;
-    it.tile = idx - bh * p.tiles;
+    uint32_t tile = (uint32_t)idx, h = p.tiles.split(tile);
+    it.tile = (int)tile;
+    it.b = (int)p.heads.split(h);
+    it.h = (int)h;
     it.len = p.keys.count(it.b);
     it.nt = (it.len + kKeys - 1) / kKeys;
     return true;
 }
 struct DqWalk {
     DqItem it;
-    int k = 0, t = 0;
-    bool ok;
-    __device__ __forceinline__ void seek(const DqP& p) {
-        while ((ok = item_at(p, k, it)) && it.nt == 0) ++k;
+    int k = -1, t = 0;
+    bool ok = true;
+    __device__ __forceinline__ DqWalk() { it.nt = 0; }
+    __device__ __forceinline__ bool next(const DqP& p) {
+        if (++t < it.nt) return true;
+        return next_item(p);
     }
-    __device__ __forceinline__ void next(const DqP& p) {
-        if (++t < it.nt) return;
-        next_item(p);
-    }
-    __device__ __forceinline__ void next_item(const DqP& p) {
+    __device__ __forceinline__ bool next_item(const DqP& p) {
         t = 0;
-        ++k;
-        seek(p);
+        do {
+            ++k;
+            ok = item_at(p, k, it);
+        } while (ok && it.nt == 0);
+        return ok;
     }
     __device__ __forceinline__ bool last() const { return t == it.nt - 1; }
 };
@@ -176,58 +178,57 @@ k_cross_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
 
     if (warp == kMmaWarp) {
         constexpr uint32_t idesc_s = instr_desc(kKeys, 0), idesc_dq = instr_desc(D, 1);
+        const uint64_t dk = smem_desc(sbase + L::offK, 16, 1024), dv = smem_desc(sbase + L::offV, 16, 1024),
+                       dk_mn = smem_desc(sbase + L::offK, L::kSlab, 1024), dqd = smem_desc(sbase + L::offQ, 16, 1024);
         uint32_t ua = 0, uc = 0;                                  // steps: scores made, dQ added
         DqWalk cur, ahead;                                        // ahead: the step whose scores are made next
-        cur.seek(prm);
-        ahead = cur;
-        auto scores = [&] {                                       // one lane
-            const uint32_t st = ua % L::kStages, buf = (ua & 1) * kKeys;
-            if (ahead.t == 0) {                                   // the item's Q and dO to TMEM
-#pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk) {
-                    const uint32_t off = (kk / 4) * L::kSlabQ + (kk % 4) * 32;
-                    cp_128x256b(tmem + L::colQ + kk * 8, smem_desc(sbase + L::offQ + off, 16, 1024));
-                    cp_128x256b(tmem + L::colDO + kk * 8, smem_desc(sbase + L::offQ + L::kQBytes + off, 16, 1024));
-                }
-                commit(bar(QD_EMPTY));
-            }
-#pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk)
-                mma_ts(tmem + L::colS + buf, tmem + L::colQ + kk * 8,
-                       smem_desc(sbase + L::offK + st * L::kTileBytes + (kk / 4) * L::kSlab + (kk % 4) * 32, 16, 1024),
-                       idesc_s, kk > 0);
-#pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk)
-                mma_ts(tmem + L::colDP + buf, tmem + L::colDO + kk * 8,
-                       smem_desc(sbase + L::offV + st * L::kTileBytes + (kk / 4) * L::kSlab + (kk % 4) * 32, 16, 1024),
-                       idesc_s, kk > 0);
-            commit(bar(S_FULL + (ua & 1)));
-            commit(bar(V_EMPTY + st));
-            if (ahead.last()) commit(bar(AB_FREE));
-        };
-        for (int i = 0; i < 2 && ahead.ok && (ok = meet(true)); ++i) {
-            fence_after();
-            if (elect_one()) scores();
-            __syncwarp();
-            ++ua;
-            ahead.next(prm);
-        }
-        for (; cur.ok && ok && (ok = meet(true)); cur.next(prm), ++uc) {
+        cur.next(prm);
+        ahead.next(prm);
+        for (int made = 0; made > 0 || ahead.ok;) {               // scores made and not yet used
+            const bool use = made == 2 || !ahead.ok, more = ahead.ok;
+            if (!(ok = meet(true))) break;
             fence_after();
             if (elect_one()) {
-                const uint32_t st = uc % L::kStages;
+                if (use) {
+                    const uint32_t st = uc % L::kStages;
 #pragma unroll
-                for (int kk = 0; kk < kKeys / 16; ++kk)
-                    mma_ts(tmem + L::colDQ, tmem + L::colS + (uc & 1) * kKeys + kk * 8,
-                           smem_desc(sbase + L::offK + st * L::kTileBytes + kk * 16 * 128, L::kSlab, 1024), idesc_dq,
-                           cur.t > 0 || kk > 0);
-                commit(bar(K_EMPTY + st));
-                if (cur.last()) commit(bar(DQ_DONE));
-                if (ahead.ok) scores();
+                    for (int kk = 0; kk < kKeys / 16; ++kk)
+                        mma_ts(tmem + L::colDQ, tmem + L::colS + (uc & 1) * kKeys + kk * 8,
+                               desc_at(dk_mn, st * L::kTileBytes + kk * 16 * 128), idesc_dq, cur.t > 0 || kk > 0);
+                    commit(bar(K_EMPTY + st));
+                    if (cur.last()) commit(bar(DQ_DONE));
+                }
+                if (more) {
+                    const uint32_t st = ua % L::kStages, buf = (ua & 1) * kKeys;
+                    if (ahead.t == 0) {                           // the item's Q and dO to TMEM
+#pragma unroll 1
+                        for (int kk = 0; kk < D / 16; ++kk) {
+                            const uint32_t off = (kk / 4) * L::kSlabQ + (kk % 4) * 32;
+                            cp_128x256b(tmem + L::colQ + kk * 8, desc_at(dqd, off));
+                            cp_128x256b(tmem + L::colDO + kk * 8, desc_at(dqd, L::kQBytes + off));
+                        }
+                        commit(bar(QD_EMPTY));
+                    }
+#pragma unroll
+                    for (int kk = 0; kk < D / 16; ++kk) {
+                        const uint32_t off = st * L::kTileBytes + (kk / 4) * L::kSlab + (kk % 4) * 32;
+                        mma_ts(tmem + L::colS + buf, tmem + L::colQ + kk * 8, desc_at(dk, off), idesc_s, kk > 0);
+                        mma_ts(tmem + L::colDP + buf, tmem + L::colDO + kk * 8, desc_at(dv, off), idesc_s, kk > 0);
+                    }
+                    commit(bar(S_FULL + (ua & 1)));
+                    commit(bar(V_EMPTY + st));
+                    if (ahead.last()) commit(bar(AB_FREE));
+                }
             }
             __syncwarp();
-            if (ahead.ok) {
+            if (use) {
+                ++uc;
+                --made;
+                cur.next(prm);
+            }
+            if (more) {
                 ++ua;
+                ++made;
                 ahead.next(prm);
             }
         }
@@ -240,35 +241,41 @@ k_cross_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
         // what each of the MMA warp's steps waits for
         uint32_t ua = 0, uc = 0, items_a = 0, items_c = 0;
         DqWalk cur, ahead;
-        cur.seek(prm);
-        ahead = cur;
-        auto scores_ready = [&] {
-            const uint32_t st = ua % L::kStages, ph = (ua / L::kStages) & 1;
-            ++ua;
-            if (!warp_wait<kEvery>(bar(K_FULL + st), ph, ctl) || !warp_wait<kEvery>(bar(V_FULL + st), ph, ctl)) return false;
-            if (ahead.t > 0) return true;
-            // Q and dO have landed, and the item before has made its last scores (a copy into TMEM is not ordered
-            // behind the products that read the same columns)
-            if (items_a > 0 && !warp_wait<kEvery>(bar(AB_FREE), (items_a - 1) & 1, ctl)) return false;
-            return warp_wait<kEvery>(bar(QD_FULL), items_a++ & 1, ctl);
-        };
-        for (int i = 0; i < 2 && ahead.ok && ok; ++i) {
-            ok = meet(scores_ready());
-            ahead.next(prm);
-        }
-        for (; cur.ok && ok; cur.next(prm), ++uc) {
-            bool go = !ahead.ok || scores_ready();
-            // dQ of the item before this one has been read
-            if (go && cur.t == 0 && items_c++ > 0) go = warp_wait<kEvery>(bar(DQ_FREE), items_c & 1, ctl);
-            ok = meet(go && warp_wait<kEvery>(bar(DS_FULL + (uc & 1)), (uc >> 1) & 1, ctl));
-            if (ahead.ok) ahead.next(prm);
+        cur.next(prm);
+        ahead.next(prm);
+        for (int made = 0; made > 0 || ahead.ok;) {
+            const bool use = made == 2 || !ahead.ok, more = ahead.ok;
+            bool go = true;
+            if (more) {
+                const uint32_t st = ua % L::kStages, ph = (ua / L::kStages) & 1;
+                go = warp_wait<kEvery>(bar(K_FULL + st), ph, ctl) && warp_wait<kEvery>(bar(V_FULL + st), ph, ctl);
+                // Q and dO have landed, and the item before has made its last scores (a copy into TMEM is not ordered
+                // behind the products that read the same columns)
+                if (ahead.t == 0) {
+                    go = go && (items_a == 0 || warp_wait<kEvery>(bar(AB_FREE), (items_a - 1) & 1, ctl)) &&
+                         warp_wait<kEvery>(bar(QD_FULL), items_a & 1, ctl);
+                    ++items_a;
+                }
+                ++ua;
+                ++made;
+                ahead.next(prm);
+            }
+            if (use) {
+                // dQ of the item before this one has been read
+                if (cur.t == 0 && items_c++ > 0) go = go && warp_wait<kEvery>(bar(DQ_FREE), items_c & 1, ctl);
+                go = go && warp_wait<kEvery>(bar(DS_FULL + (uc & 1)), (uc >> 1) & 1, ctl);
+                ++uc;
+                --made;
+                cur.next(prm);
+            }
+            if (!(ok = meet(go))) break;
         }
         if (!ok && lane == 0) { ctl->abort = 1; record_error(prm.err, BSA_EDEVICE, -3); }
     } else if (warp == kPollWarp + 1) {
         // K ring.  dQ += dS K: rows of states that do not count become zeros (0 * NaN is NaN)
         uint32_t u = 0, raw = 0;
         DqWalk w;
-        for (w.seek(prm); w.ok; w.next(prm), ++u) {
+        for (; w.next(prm); ++u) {
             const int st = u % L::kStages;
             if (u >= L::kStages && !(ok = warp_sleep<kEvery>(bar(K_EMPTY + st), (u / L::kStages - 1) & 1, ctl))) break;
             uint32_t bits[2];
@@ -278,7 +285,7 @@ k_cross_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
             if (lane == 0) {
                 mbar_expect_tx(full, L::kTileBytes);
                 for (int s = 0; s < D / 64; ++s)
-                    tma_load_4d(dst + s * L::kSlab, &tmK, s * 64, w.t * kKeys, w.it.h / prm.G, w.it.b, full);
+                    tma_load_4d(dst + s * L::kSlab, &tmK, s * 64, w.t * kKeys, (int)prm.G.quot(w.it.h), w.it.b, full);
             }
             if (fix) {
                 if (!warp_wait<kEvery>(full, raw & 1, ctl)) {
@@ -287,10 +294,7 @@ k_cross_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
                     break;
                 }
                 ++raw;
-                for (int i = 0; i < kKeys; ++i)
-                    if (!(bits[i / 32] >> (i % 32) & 1) && lane < D / 8)
-                        *reinterpret_cast<uint4*>(smem + (dst - sbase) + (lane / 8) * L::kSlab + i * 128 +
-                                                  (lane % 8) * 16) = make_uint4(0, 0, 0, 0);
+                zero_rows<D>(smem + (dst - sbase), bits, lane);
                 fence_proxy_async();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(K_FULL + st));
@@ -303,13 +307,13 @@ k_cross_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
         if (lane == 0) {
             uint32_t u = 0;
             DqWalk w;
-            for (w.seek(prm); w.ok; w.next(prm), ++u) {
+            for (; w.next(prm); ++u) {
                 const int st = u % L::kStages;
                 if (u >= L::kStages && !(ok = mbar_sleep<kEvery>(bar(V_EMPTY + st), (u / L::kStages - 1) & 1, ctl))) break;
                 mbar_expect_tx(bar(V_FULL + st), L::kTileBytes);
                 for (int s = 0; s < D / 64; ++s)
                     tma_load_4d(sbase + L::offV + st * L::kTileBytes + s * L::kSlab, &tmV, s * 64, w.t * kKeys,
-                                w.it.h / prm.G, w.it.b, bar(V_FULL + st));
+                                (int)prm.G.quot(w.it.h), w.it.b, bar(V_FULL + st));
             }
             if (!ok) { ctl->abort = 1; record_error(prm.err, BSA_EDEVICE, -2); }
             for (uint32_t st = 0; st < L::kStages; ++st)
@@ -339,32 +343,36 @@ k_cross_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
                 uint32_t sv[2][16], dv[2][16];
                 tmem_ld16(ts, sv[0]);
                 tmem_ld16(tp, dv[0]);
+#pragma unroll 1
+                for (int half = 0; half < 2; ++half) {
+                    const uint32_t word = half ? bits[1] : bits[0];
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    tmem_wait_ld();
-                    if (c < 3) {
-                        tmem_ld16(ts + (c + 1) * 16, sv[(c + 1) & 1]);
-                        tmem_ld16(tp + (c + 1) * 16, dv[(c + 1) & 1]);
-                    }
-                    const uint32_t *x = sv[c & 1], *dp = dv[c & 1];
-                    uint32_t pk[8];
+                    for (int i = 0; i < 2; ++i) {
+                        const int c = 2 * half + i;
+                        tmem_wait_ld();
+                        if (c < 3) {
+                            tmem_ld16(ts + (c + 1) * 16, sv[i ^ 1]);
+                            tmem_ld16(tp + (c + 1) * 16, dv[i ^ 1]);
+                        }
+                        uint32_t pk[8];
 #pragma unroll
-                    for (int e = 0; e < 16; e += 2) {
-                        float x0, x1, d0, d1;
-                        ffma2(x0, x1, __uint_as_float(x[e]), __uint_as_float(x[e + 1]), prm.scale_log2, prm.scale_log2,
-                              neg_lse, neg_lse);
-                        fadd2(d0, d1, __uint_as_float(dp[e]), __uint_as_float(dp[e + 1]), neg_d, neg_d);
-                        const float p0 = ex2_mufu(x0), p1 = ex2_mufu(x1);
-                        fmul2(d0, d1, d0, d1, p0, p1);
-                        pk[e / 2] = pack_bf16(d0, d1);
-                    }
-                    if (!all) {
-                        const uint32_t on = bits[c / 2] >> (16 * (c & 1));
+                        for (int e = 0; e < 16; e += 2) {
+                            float x0, x1, d0, d1;
+                            ffma2(x0, x1, __uint_as_float(sv[i][e]), __uint_as_float(sv[i][e + 1]), prm.scale_log2,
+                                  prm.scale_log2, neg_lse, neg_lse);
+                            fadd2(d0, d1, __uint_as_float(dv[i][e]), __uint_as_float(dv[i][e + 1]), neg_d, neg_d);
+                            const float p0 = ex2_mufu(x0), p1 = ex2_mufu(x1);
+                            fmul2(d0, d1, d0, d1, p0, p1);
+                            pk[e / 2] = pack_bf16(d0, d1);
+                        }
+                        if (!all) {
+                            const uint32_t on = word >> (16 * i);
 #pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            pk[e] &= (on >> (2 * e) & 1 ? 0xffffu : 0u) | (on >> (2 * e + 1) & 1 ? 0xffff0000u : 0u);
+                            for (int e = 0; e < 8; ++e)
+                                pk[e] &= (on >> (2 * e) & 1 ? 0xffffu : 0u) | (on >> (2 * e + 1) & 1 ? 0xffff0000u : 0u);
+                        }
+                        tmem_st8(ts + c * 8, pk);
                     }
-                    tmem_st8(ts + c * 8, pk);
                 }
                 tmem_wait_st();
                 fence_before();
@@ -403,33 +411,31 @@ k_cross_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
             constexpr int kLanes = D / 8, kPer = 32 / kLanes;
             const int sub = lane / kLanes, c = lane % kLanes, n0 = it.tile * kTile + 32 * quad;
             const int64_t at = (((int64_t)it.b * prm.N + n0) * prm.H + it.h) * D + c * 8;
-            float t[kLanes];                                          // this lane's part of row i * kPer + sub
-#pragma unroll
+            // four rows of each group of kLanes lanes at a time; the sums over a row's lanes carry half as many values
+            // after each of the first two steps
+            float d = 0.f;
+#pragma unroll 1
             for (int i0 = 0; i0 < kLanes; i0 += 4) {
-                uint4 ov[4], gv[4];
+                float t[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int rr = (i0 + i) * kPer + sub;
                     const int64_t e = at + (int64_t)rr * prm.H * D;
+                    const uint4 zero = make_uint4(0, 0, 0, 0);
                     const bool in = n0 + rr < prm.N;
-                    ov[i] = in ? __ldg(reinterpret_cast<const uint4*>(prm.o + e)) : make_uint4(0, 0, 0, 0);
-                    gv[i] = in ? __ldg(reinterpret_cast<const uint4*>(prm.d_o + e)) : make_uint4(0, 0, 0, 0);
+                    t[i] = dot8(in ? __ldg(reinterpret_cast<const uint4*>(prm.o + e)) : zero,
+                                in ? __ldg(reinterpret_cast<const uint4*>(prm.d_o + e)) : zero);
                 }
+                const bool u2 = c & (kLanes / 2), u1 = c & (kLanes / 4);
+                const float a = (u2 ? t[2] : t[0]) + __shfl_xor_sync(0xffffffffu, u2 ? t[0] : t[2], kLanes / 2);
+                const float b = (u2 ? t[3] : t[1]) + __shfl_xor_sync(0xffffffffu, u2 ? t[1] : t[3], kLanes / 2);
+                float v = (u1 ? b : a) + __shfl_xor_sync(0xffffffffu, u1 ? a : b, kLanes / 4);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) t[i0 + i] = dot8(ov[i], gv[i]);
+                for (int x = kLanes / 8; x > 0; x >>= 1) v += __shfl_xor_sync(0xffffffffu, v, x);
+                // row (i0 + i) kPer + sub is in lane sub kLanes + i kLanes / 4: to the lane of its number
+                const float got = __shfl_sync(0xffffffffu, v, (lane % kPer) * kLanes + (lane / kPer) % 4 * (kLanes / 4));
+                if (lane / (4 * kPer) == i0 / 4) d = got;
             }
-            // sums over a row's lanes, half as many values carried after each step (shuffles share the path that the
-            // products' operands saturate: 80 of them took 8000 cycles here); lane c ends with i = c
-#pragma unroll
-            for (int x = kLanes / 2; x > 0; x >>= 1) {
-                const bool up = c & x;
-#pragma unroll
-                for (int i = 0; i < x; ++i) {
-                    const float keep = up ? t[i + x] : t[i], give = up ? t[i] : t[i + x];
-                    t[i] = keep + __shfl_xor_sync(0xffffffffu, give, x);
-                }
-            }
-            const float d = __shfl_sync(0xffffffffu, t[0], (lane % kPer) * kLanes + lane / kPer);
             float lse2 = 0.f;
             const int n = n0 + lane;
             if (n < prm.N) {
@@ -447,18 +453,13 @@ k_cross_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
             return true;
         };
         DqWalk pre;
-        pre.seek(prm);
-        if (pre.ok) {
-            ok = load(pre.it) && rows(pre.it);
-            pre.next_item(prm);
-        }
         DqItem it;
-        for (int k = 0; ok && item_at(prm, k, it); ++k) {
-            if (it.nt > 0) {
-                if (pre.ok) {                                         // the next item's D before this one's dQ
-                    if (!(ok = load(pre.it) && rows(pre.it))) break;
-                    pre.next_item(prm);
-                }
+        // k = -1: the first item's rows only
+        for (int k = -1; k < 0 || item_at(prm, k, it); ++k) {
+            if (k < 0 || it.nt > 0) {
+                // the next item's D before this one's dQ
+                if (pre.ok && pre.next_item(prm) && !(ok = load(pre.it) && rows(pre.it))) break;
+                if (k < 0) continue;
                 if (!(ok = warp_sleep<kEvery>(bar(DQ_DONE), nd & 1, ctl))) break;
                 ++nd;
                 fence_after();
@@ -485,7 +486,7 @@ k_cross_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
                 if (lane == 0) mbar_arrive(bar(DQ_FREE));
             }
 #pragma unroll
-            for (int s = 0; s < D / 64; ++s) {
+            for (int s = 0; s < D / 64; ++s) {                        // unrolled: pk stays in registers
                 if (lane == 0) bulk_wait_read();
                 __syncwarp();
 #pragma unroll
@@ -518,7 +519,9 @@ struct DkvP {
     float* part;                     // [2: dK, dV][chunks][B, M, Hkv, D], or null: dk, dv hold the result
     __nv_bfloat16 *dk, *dv;
     int32_t* err;
-    int N, H, G, B, Hkv, key_tiles, chunks, nq, items;
+    int N, H, G, Hkv, chunks, nq, items;
+    int share, extra;                // steps of a share, of which the first `extra` have one more
+    Div key_tiles, shares, key_heads, nqd;
     int64_t part_stride;             // floats of one chunk: B * M * Hkv * D
     float scale, scale_log2;
     unsigned long long wait_ns;
@@ -542,35 +545,34 @@ struct DkvItem {
     int b, hk, kt, chunk, len, beg, end;      // steps [beg, end); none if the tile has no valid state
 };
 __device__ __forceinline__ bool item_at(const DkvP& p, int k, DkvItem& it) {
-    int idx = k * gridDim.x + blockIdx.x;
+    const int idx = k * gridDim.x + blockIdx.x;
     if (idx >= p.items) return false;
-    it.kt = idx % p.key_tiles;
-    idx /= p.key_tiles;
-    it.chunk = idx % p.chunks;
-    idx /= p.chunks;
-    it.hk = idx % p.Hkv;
-    it.b = idx / p.Hkv;
+    uint32_t kt = (uint32_t)idx, c = p.key_tiles.split(kt), hk = p.shares.split(c);
+    it.kt = (int)kt;
+    it.chunk = (int)c;
+    it.b = (int)p.key_heads.split(hk);
+    it.hk = (int)hk;
     it.len = p.keys.count(it.b);
-    const int64_t steps = (int64_t)p.G * p.nq;
-    it.beg = (int)(steps * it.chunk / p.chunks);
-    it.end = it.kt * kTile < it.len ? (int)(steps * (it.chunk + 1) / p.chunks) : it.beg;
+    it.beg = p.share * it.chunk + min(it.chunk, p.extra);
+    it.end = it.kt * kTile < it.len ? it.beg + p.share + (it.chunk < p.extra) : it.beg;
     return true;
 }
 struct DkvWalk {
     DkvItem it;
-    int k = 0, s = 0;
-    bool ok;
-    __device__ __forceinline__ void seek(const DkvP& p) {
-        while ((ok = item_at(p, k, it)) && it.end == it.beg) ++k;
+    int k = -1, s = 0;
+    bool ok = true;
+    __device__ __forceinline__ DkvWalk() { it.beg = it.end = 0; }
+    __device__ __forceinline__ bool next(const DkvP& p) {
+        if (++s < it.end) return true;
+        return next_item(p);
+    }
+    __device__ __forceinline__ bool next_item(const DkvP& p) {
+        do {
+            ++k;
+            ok = item_at(p, k, it);
+        } while (ok && it.end == it.beg);
         s = it.beg;
-    }
-    __device__ __forceinline__ void next(const DkvP& p) {
-        if (++s < it.end) return;
-        next_item(p);
-    }
-    __device__ __forceinline__ void next_item(const DkvP& p) {
-        ++k;
-        seek(p);
+        return ok;
     }
     __device__ __forceinline__ bool first() const { return s == it.beg; }
     __device__ __forceinline__ bool last() const { return s == it.end - 1; }
@@ -602,50 +604,51 @@ k_cross_dkv(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUt
 
     if (warp == kMmaWarp) {
         constexpr uint32_t idesc_s = instr_desc(kKeys, 0), idesc_g = instr_desc(D, 1);
+        const uint64_t dk = smem_desc(sbase + L::offK, 16, 1024), dq = smem_desc(sbase + L::offQ, 16, 1024),
+                       dq_mn = smem_desc(sbase + L::offQ, L::kSlab, 1024);
         uint32_t ua = 0, uc = 0;
         DkvWalk cur, ahead;
-        cur.seek(prm);
-        ahead = cur;
-        auto scores = [&] {                                       // one lane
-            const uint32_t buf = (ua & 1) * kKeys, q = sbase + L::offQ + ua % L::kStages * 2 * L::kTileBytes;
-#pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk)
-                mma_ss(tmem + L::colS + buf, smem_desc(sbase + L::offK + (kk / 4) * L::kSlabK + (kk % 4) * 32, 16, 1024),
-                       smem_desc(q + (kk / 4) * L::kSlab + (kk % 4) * 32, 16, 1024), idesc_s, kk > 0);
-#pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk)
-                mma_ss(tmem + L::colDP + buf,
-                       smem_desc(sbase + L::offK + L::kKBytes + (kk / 4) * L::kSlabK + (kk % 4) * 32, 16, 1024),
-                       smem_desc(q + L::kTileBytes + (kk / 4) * L::kSlab + (kk % 4) * 32, 16, 1024), idesc_s, kk > 0);
-            commit(bar(S_FULL + (ua & 1)));
-            if (ahead.last()) commit(bar(KV_EMPTY));
-        };
-        for (int i = 0; i < 2 && ahead.ok && (ok = meet(true)); ++i) {
-            fence_after();
-            if (elect_one()) scores();
-            __syncwarp();
-            ++ua;
-            ahead.next(prm);
-        }
-        for (; cur.ok && ok && (ok = meet(true)); cur.next(prm), ++uc) {
+        cur.next(prm);
+        ahead.next(prm);
+        for (int made = 0; made > 0 || ahead.ok;) {
+            const bool use = made == 2 || !ahead.ok, more = ahead.ok;
+            if (!(ok = meet(true))) break;
             fence_after();
             if (elect_one()) {
-                const uint32_t st = uc % L::kStages, q = sbase + L::offQ + st * 2 * L::kTileBytes, buf = (uc & 1) * kKeys;
+                if (use) {
+                    const uint32_t st = uc % L::kStages, q = st * 2 * L::kTileBytes, buf = (uc & 1) * kKeys;
 #pragma unroll
-                for (int kk = 0; kk < kKeys / 16; ++kk)
-                    mma_ts(tmem + L::colDV, tmem + L::colS + buf + kk * 8,
-                           smem_desc(q + L::kTileBytes + kk * 16 * 128, L::kSlab, 1024), idesc_g, !cur.first() || kk > 0);
+                    for (int kk = 0; kk < kKeys / 16; ++kk) {
+                        mma_ts(tmem + L::colDV, tmem + L::colS + buf + kk * 8,
+                               desc_at(dq_mn, q + L::kTileBytes + kk * 16 * 128), idesc_g, !cur.first() || kk > 0);
+                        mma_ts(tmem + L::colDK, tmem + L::colDP + buf + kk * 8, desc_at(dq_mn, q + kk * 16 * 128), idesc_g,
+                               !cur.first() || kk > 0);
+                    }
+                    commit(bar(ST_EMPTY + st));
+                    if (cur.last()) commit(bar(ACC_DONE));
+                }
+                if (more) {
+                    const uint32_t buf = (ua & 1) * kKeys, q = ua % L::kStages * 2 * L::kTileBytes;
 #pragma unroll
-                for (int kk = 0; kk < kKeys / 16; ++kk)
-                    mma_ts(tmem + L::colDK, tmem + L::colDP + buf + kk * 8, smem_desc(q + kk * 16 * 128, L::kSlab, 1024),
-                           idesc_g, !cur.first() || kk > 0);
-                commit(bar(ST_EMPTY + st));
-                if (cur.last()) commit(bar(ACC_DONE));
-                if (ahead.ok) scores();
+                    for (int kk = 0; kk < D / 16; ++kk) {
+                        const uint32_t ok_ = (kk / 4) * L::kSlabK + (kk % 4) * 32, oq = q + (kk / 4) * L::kSlab + (kk % 4) * 32;
+                        mma_ss(tmem + L::colS + buf, desc_at(dk, ok_), desc_at(dq, oq), idesc_s, kk > 0);
+                        mma_ss(tmem + L::colDP + buf, desc_at(dk, L::kKBytes + ok_), desc_at(dq, L::kTileBytes + oq), idesc_s,
+                               kk > 0);
+                    }
+                    commit(bar(S_FULL + (ua & 1)));
+                    if (ahead.last()) commit(bar(KV_EMPTY));
+                }
             }
             __syncwarp();
-            if (ahead.ok) {
+            if (use) {
+                ++uc;
+                --made;
+                cur.next(prm);
+            }
+            if (more) {
                 ++ua;
+                ++made;
                 ahead.next(prm);
             }
         }
@@ -657,32 +660,36 @@ k_cross_dkv(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUt
     } else if (warp == kPollWarp) {
         uint32_t ua = 0, uc = 0, items_a = 0, items_c = 0;
         DkvWalk cur, ahead;
-        cur.seek(prm);
-        ahead = cur;
-        auto scores_ready = [&] {
-            const uint32_t st = ua % L::kStages, ph = (ua / L::kStages) & 1;
-            ++ua;
-            return warp_wait<kEvery>(bar(ST_FULL + st), ph, ctl) &&
-                   (!ahead.first() || warp_wait<kEvery>(bar(KV_FULL), items_a++ & 1, ctl));
-        };
-        for (int i = 0; i < 2 && ahead.ok && ok; ++i) {
-            ok = meet(scores_ready());
-            ahead.next(prm);
-        }
-        for (; cur.ok && ok; cur.next(prm), ++uc) {
-            bool go = !ahead.ok || scores_ready();
-            // dK and dV of the item before this one have been read
-            if (go && cur.first() && items_c++ > 0) go = warp_wait<kEvery>(bar(ACC_FREE), items_c & 1, ctl);
-            ok = meet(go && warp_wait<kEvery>(bar(PD_FULL + (uc & 1)), (uc >> 1) & 1, ctl));
-            if (ahead.ok) ahead.next(prm);
+        cur.next(prm);
+        ahead.next(prm);
+        for (int made = 0; made > 0 || ahead.ok;) {
+            const bool use = made == 2 || !ahead.ok, more = ahead.ok;
+            bool go = true;
+            if (more) {
+                go = warp_wait<kEvery>(bar(ST_FULL + ua % L::kStages), (ua / L::kStages) & 1, ctl);
+                if (ahead.first()) go = go && warp_wait<kEvery>(bar(KV_FULL), items_a++ & 1, ctl);
+                ++ua;
+                ++made;
+                ahead.next(prm);
+            }
+            if (use) {
+                // dK and dV of the item before this one have been read
+                if (cur.first() && items_c++ > 0) go = go && warp_wait<kEvery>(bar(ACC_FREE), items_c & 1, ctl);
+                go = go && warp_wait<kEvery>(bar(PD_FULL + (uc & 1)), (uc >> 1) & 1, ctl);
+                ++uc;
+                --made;
+                cur.next(prm);
+            }
+            if (!(ok = meet(go))) break;
         }
         if (!ok && lane == 0) { ctl->abort = 1; record_error(prm.err, BSA_EDEVICE, -3); }
     } else if (warp == kPollWarp + 1) {
         uint32_t u = 0;
         DkvWalk w;
-        for (w.seek(prm); w.ok; w.next(prm), ++u) {
+        for (; w.next(prm); ++u) {
             const int st = u % L::kStages;
-            const int h = w.it.hk * prm.G + w.s / prm.nq, q0 = w.s % prm.nq * kKeys;
+            uint32_t tile = (uint32_t)w.s;
+            const int h = w.it.hk * prm.G + (int)prm.nqd.split(tile), q0 = (int)tile * kKeys;
             float l[2], d[2];                            // rows past N: lse = inf, so P is 0
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
@@ -715,7 +722,7 @@ k_cross_dkv(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUt
         if (lane == 0) {
             uint32_t n = 0;
             DkvWalk w;
-            for (w.seek(prm); w.ok; w.next_item(prm), ++n) {
+            for (; w.next_item(prm); ++n) {
                 if (n > 0 && !(ok = mbar_sleep<kEvery>(bar(KV_EMPTY), (n - 1) & 1, ctl))) break;
                 mbar_expect_tx(bar(KV_FULL), 2 * L::kKBytes);
                 for (int s = 0; s < D / 64; ++s) {
@@ -733,8 +740,7 @@ k_cross_dkv(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUt
         const uint32_t ts = tmem + ((uint32_t)(32 * quad) << 16) + L::colS + g * kKeys, tp = ts - L::colS + L::colDP;
         uint32_t u = 0;
         DkvWalk w;
-        w.seek(prm);
-        for (; w.ok; w.next_item(prm)) {
+        while (w.next_item(prm)) {
             const int j = w.it.kt * kTile + 32 * quad + lane;         // this thread's key
             const bool on = j < w.it.len && (!prm.keys.key_mask || prm.keys.key_mask[(int64_t)w.it.b * prm.keys.M + j]);
             for (int s = w.it.beg; s < w.it.end; ++s, ++u) {
@@ -747,39 +753,38 @@ k_cross_dkv(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUt
                 uint32_t sv[2][16], dv[2][16];
                 tmem_ld16(ts, sv[0]);
                 tmem_ld16(tp, dv[0]);
+#pragma unroll 1
+                for (int half = 0; half < 2; ++half)
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    tmem_wait_ld();
-                    if (c < 3) {
-                        tmem_ld16(ts + (c + 1) * 16, sv[(c + 1) & 1]);
-                        tmem_ld16(tp + (c + 1) * 16, dv[(c + 1) & 1]);
-                    }
-                    const uint32_t *x = sv[c & 1], *dp = dv[c & 1];
-                    uint32_t pk[8], dk[8];
-#pragma unroll
-                    for (int e = 0; e < 16; e += 4) {
-                        const float4 l4 = *reinterpret_cast<const float4*>(rv + c * 16 + e);
-                        const float4 d4 = *reinterpret_cast<const float4*>(rv + kKeys + c * 16 + e);
-                        const float l[4] = {l4.x, l4.y, l4.z, l4.w}, d[4] = {d4.x, d4.y, d4.z, d4.w};
-#pragma unroll
-                        for (int f = 0; f < 4; f += 2) {
-                            float x0, x1, d0, d1;
-                            ffma2(x0, x1, __uint_as_float(x[e + f]), __uint_as_float(x[e + f + 1]), prm.scale_log2,
-                                  prm.scale_log2, l[f], l[f + 1]);
-                            fadd2(d0, d1, __uint_as_float(dp[e + f]), __uint_as_float(dp[e + f + 1]), d[f], d[f + 1]);
-                            const float p0 = ex2_mufu(x0), p1 = ex2_mufu(x1);
-                            fmul2(d0, d1, d0, d1, p0, p1);
-                            pk[(e + f) / 2] = pack_bf16(p0, p1);
-                            dk[(e + f) / 2] = pack_bf16(d0, d1);
+                    for (int i = 0; i < 2; ++i) {
+                        const int c = 2 * half + i;
+                        tmem_wait_ld();
+                        if (c < 3) {
+                            tmem_ld16(ts + (c + 1) * 16, sv[i ^ 1]);
+                            tmem_ld16(tp + (c + 1) * 16, dv[i ^ 1]);
                         }
-                    }
-                    if (!on) {
+                        uint32_t pk[8], dk[8];
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) pk[e] = dk[e] = 0u;
+                        for (int e = 0; e < 16; e += 4) {
+                            const float4 l4 = *reinterpret_cast<const float4*>(rv + c * 16 + e);
+                            const float4 d4 = *reinterpret_cast<const float4*>(rv + kKeys + c * 16 + e);
+                            const float l[4] = {l4.x, l4.y, l4.z, l4.w}, d[4] = {d4.x, d4.y, d4.z, d4.w};
+#pragma unroll
+                            for (int f = 0; f < 4; f += 2) {
+                                float x0, x1, d0, d1;
+                                ffma2(x0, x1, __uint_as_float(sv[i][e + f]), __uint_as_float(sv[i][e + f + 1]),
+                                      prm.scale_log2, prm.scale_log2, l[f], l[f + 1]);
+                                fadd2(d0, d1, __uint_as_float(dv[i][e + f]), __uint_as_float(dv[i][e + f + 1]), d[f],
+                                      d[f + 1]);
+                                const float p0 = ex2_mufu(x0), p1 = ex2_mufu(x1);
+                                fmul2(d0, d1, d0, d1, p0, p1);
+                                pk[(e + f) / 2] = on ? pack_bf16(p0, p1) : 0u;
+                                dk[(e + f) / 2] = on ? pack_bf16(d0, d1) : 0u;
+                            }
+                        }
+                        tmem_st8(ts + c * 8, pk);
+                        tmem_st8(tp + c * 8, dk);
                     }
-                    tmem_st8(ts + c * 8, pk);
-                    tmem_st8(tp + c * 8, dk);
-                }
                 tmem_wait_st();
                 fence_before();
                 __syncwarp();
@@ -950,9 +955,11 @@ cudaError_t launch_cross_bwd_tc(const bsa_plan& p, const CrossArgs& a, const voi
     pq.err = p.d_err;
     pq.N = (int)p.N;
     pq.H = p.H;
-    pq.G = p.H / a.Hkv;
-    pq.tiles = (int)((p.N + kTile - 1) / kTile);
-    pq.items = p.B * p.H * pq.tiles;
+    pq.heads = Div(p.H);
+    pq.G = Div(p.H / a.Hkv);
+    const int tiles = (int)((p.N + kTile - 1) / kTile);
+    pq.tiles = Div(tiles);
+    pq.items = p.B * p.H * tiles;
     pq.scale = 1.f / sqrtf((float)p.d);
     pq.scale_log2 = kLog2e * pq.scale;
     pq.wait_ns = p.wait_ns;
@@ -965,10 +972,16 @@ cudaError_t launch_cross_bwd_tc(const bsa_plan& p, const CrossArgs& a, const voi
     pk.dk = (__nv_bfloat16*)dk;
     pk.dv = (__nv_bfloat16*)dv;
     pk.err = p.d_err;
-    pk.N = pq.N; pk.H = p.H; pk.G = pq.G; pk.B = p.B; pk.Hkv = a.Hkv;
-    pk.key_tiles = (int)((a.M + kTile - 1) / kTile);
+    pk.N = pq.N; pk.H = p.H; pk.G = p.H / a.Hkv; pk.Hkv = a.Hkv;
+    const int key_tiles = (int)((a.M + kTile - 1) / kTile);
     pk.nq = (int)((p.N + kKeys - 1) / kKeys);
-    pk.items = p.B * a.Hkv * pk.key_tiles * pk.chunks;
+    pk.share = (int)((int64_t)pk.G * pk.nq / pk.chunks);
+    pk.extra = (int)((int64_t)pk.G * pk.nq % pk.chunks);
+    pk.key_tiles = Div(key_tiles);
+    pk.shares = Div(pk.chunks);
+    pk.key_heads = Div(a.Hkv);
+    pk.nqd = Div(pk.nq);
+    pk.items = p.B * a.Hkv * key_tiles * pk.chunks;
     pk.part_stride = (int64_t)p.B * a.M * a.Hkv * p.d;
     pk.scale = pq.scale; pk.scale_log2 = pq.scale_log2;
     pk.wait_ns = p.wait_ns;
