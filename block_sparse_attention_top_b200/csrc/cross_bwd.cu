@@ -12,10 +12,13 @@
 // depends on scheduling.  A third kernel adds the key side's shares in order.
 //
 // Both passes work in tiles of 64 on the side they walk, with two buffers of
-// S and dP in TMEM; softmax group 0 (warps 0-3) takes the even tiles and
-// group 1 (warps 4-7) the odd ones, a thread per row of the owned side.  P and
-// dS (bf16) overwrite the S and dP that their thread has read.  The tensor
-// cores make S and dP of tile u+2 behind the products that read tile u.
+// S and dP in TMEM.  Each of the softmax warps 0-3 and 4-7 takes half of every
+// tile's columns, a thread per row of the owned side (no sum runs along a row:
+// lse and D are given); P and dS (bf16) overwrite the columns that their
+// thread has read, so the A operand of a product is two runs of 16 columns.
+// The tensor cores make S and dP of tile u+2 behind the products that read
+// tile u.  (Taking turns, each group a whole tile, the softmax of a tile took
+// 1500 cycles, longer than the tensor cores' 1400 for the tile between.)
 //
 // Waits are bounded as in attn_pp.cu.
 #include <algorithm>
@@ -102,12 +105,13 @@ template <int D>
 struct DqSmem {
     static constexpr int kSlabQ = kTile * 128, kSlab = kKeys * 128;
     static constexpr int kQBytes = kTile * D * 2, kTileBytes = kKeys * D * 2;
-    static constexpr int kStages = 4;
+    static constexpr int kStages = 4, kStagesV = 3;                // a K tile is used once more than a V tile
     static constexpr int offQ = 0;                                 // Q, dO
     static constexpr int offK = offQ + 2 * kQBytes;
     static constexpr int offV = offK + kStages * kTileBytes;
-    static constexpr int offOut = offV + kStages * kTileBytes;     // 4 warps x 32 rows x 64 columns
-    static constexpr int offRows = offOut + 4 * 4096;              // float lse, D [2 items][128]
+    static constexpr int kOutBytes = 32 * D * 2;
+    static constexpr int offOut = offV + kStagesV * kTileBytes;    // 4 warps x 32 rows x D columns
+    static constexpr int offRows = offOut + 4 * kOutBytes;         // float lse, D [2 items][128]
     static constexpr int offBar = offRows + 2 * 2 * kTile * 4;
     static constexpr int offMisc = offBar + 48 * 8;
     static constexpr int kAlloc = offMisc + 64 + 1024;
@@ -157,7 +161,7 @@ k_cross_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
     enum {
         QD_FULL = 0, QD_EMPTY, AB_FREE, S_FULL, DS_FULL = S_FULL + 2, ROWS_FULL = DS_FULL + 2, ROWS_EMPTY = ROWS_FULL + 2,
         DQ_DONE = ROWS_EMPTY + 2, DQ_FREE, DRAIN, K_RAW, K_FULL, K_EMPTY = K_FULL + L::kStages,
-        V_FULL = K_EMPTY + L::kStages, V_EMPTY = V_FULL + L::kStages, kBars = V_EMPTY + L::kStages
+        V_FULL = K_EMPTY + L::kStages, V_EMPTY = V_FULL + L::kStagesV, kBars = V_EMPTY + L::kStagesV
     };
     static_assert(kBars <= 48, "barrier slots");
     extern __shared__ __align__(1024) unsigned char smem_raw[];
@@ -169,8 +173,8 @@ k_cross_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
     float* row_vals = reinterpret_cast<float*>(smem + L::offRows);
     const uint32_t tmem = begin_cta<kBars>(bar(0), ctl, reinterpret_cast<uint32_t*>(smem + L::offMisc + 16), prm.wait_ns,
                                            [](int i) -> uint32_t {
-                                               if (i == ROWS_EMPTY || i == ROWS_EMPTY + 1) return 8;
-                                               if ((i >= DS_FULL && i < ROWS_EMPTY) || i == DQ_FREE) return 4;
+                                               if ((i >= DS_FULL && i < DS_FULL + 2) || (i >= ROWS_EMPTY && i < ROWS_EMPTY + 2)) return 8;
+                                               if ((i >= ROWS_FULL && i < ROWS_FULL + 2) || i == DQ_FREE) return 4;
                                                return 1;
                                            });
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
@@ -182,10 +186,13 @@ k_cross_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
                        dk_mn = smem_desc(sbase + L::offK, L::kSlab, 1024), dqd = smem_desc(sbase + L::offQ, 16, 1024);
         uint32_t ua = 0, uc = 0;                                  // steps: scores made, dQ added
         DqWalk cur, ahead;                                        // ahead: the step whose scores are made next
-        cur.next(prm);
-        ahead.next(prm);
-        for (int made = 0; made > 0 || ahead.ok;) {               // scores made and not yet used
-            const bool use = made == 2 || !ahead.ok, more = ahead.ok;
+        bool use = true, more = true;
+        for (int made = 0;;) {                                    // scores made and not yet used
+            if (more) ahead.next(prm);
+            if (use) cur.next(prm);
+            if (made == 0 && !ahead.ok) break;
+            use = made == 2 || !ahead.ok;
+            more = ahead.ok;
             if (!(ok = meet(true))) break;
             fence_after();
             if (elect_one()) {
@@ -193,13 +200,13 @@ k_cross_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
                     const uint32_t st = uc % L::kStages;
 #pragma unroll
                     for (int kk = 0; kk < kKeys / 16; ++kk)
-                        mma_ts(tmem + L::colDQ, tmem + L::colS + (uc & 1) * kKeys + kk * 8,
+                        mma_ts(tmem + L::colDQ, tmem + L::colS + (uc & 1) * kKeys + (kk / 2) * 32 + (kk % 2) * 8,
                                desc_at(dk_mn, st * L::kTileBytes + kk * 16 * 128), idesc_dq, cur.t > 0 || kk > 0);
                     commit(bar(K_EMPTY + st));
                     if (cur.last()) commit(bar(DQ_DONE));
                 }
                 if (more) {
-                    const uint32_t st = ua % L::kStages, buf = (ua & 1) * kKeys;
+                    const uint32_t st = ua % L::kStages, sv = ua % L::kStagesV, buf = (ua & 1) * kKeys;
                     if (ahead.t == 0) {                           // the item's Q and dO to TMEM
 #pragma unroll 1
                         for (int kk = 0; kk < D / 16; ++kk) {
@@ -211,26 +218,21 @@ k_cross_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
                     }
 #pragma unroll
                     for (int kk = 0; kk < D / 16; ++kk) {
-                        const uint32_t off = st * L::kTileBytes + (kk / 4) * L::kSlab + (kk % 4) * 32;
-                        mma_ts(tmem + L::colS + buf, tmem + L::colQ + kk * 8, desc_at(dk, off), idesc_s, kk > 0);
-                        mma_ts(tmem + L::colDP + buf, tmem + L::colDO + kk * 8, desc_at(dv, off), idesc_s, kk > 0);
+                        const uint32_t off = (kk / 4) * L::kSlab + (kk % 4) * 32;
+                        mma_ts(tmem + L::colS + buf, tmem + L::colQ + kk * 8, desc_at(dk, st * L::kTileBytes + off), idesc_s,
+                               kk > 0);
+                        mma_ts(tmem + L::colDP + buf, tmem + L::colDO + kk * 8, desc_at(dv, sv * L::kTileBytes + off),
+                               idesc_s, kk > 0);
                     }
                     commit(bar(S_FULL + (ua & 1)));
-                    commit(bar(V_EMPTY + st));
+                    commit(bar(V_EMPTY + sv));
                     if (ahead.last()) commit(bar(AB_FREE));
                 }
             }
             __syncwarp();
-            if (use) {
-                ++uc;
-                --made;
-                cur.next(prm);
-            }
-            if (more) {
-                ++ua;
-                ++made;
-                ahead.next(prm);
-            }
+            uc += use;
+            ua += more;
+            made += (int)more - (int)use;
         }
         if (elect_one()) {
             commit(bar(DRAIN));
@@ -241,14 +243,17 @@ k_cross_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
         // what each of the MMA warp's steps waits for
         uint32_t ua = 0, uc = 0, items_a = 0, items_c = 0;
         DqWalk cur, ahead;
-        cur.next(prm);
-        ahead.next(prm);
-        for (int made = 0; made > 0 || ahead.ok;) {
-            const bool use = made == 2 || !ahead.ok, more = ahead.ok;
+        bool use = true, more = true;
+        for (int made = 0;;) {
+            if (more) ahead.next(prm);
+            if (use) cur.next(prm);
+            if (made == 0 && !ahead.ok) break;
+            use = made == 2 || !ahead.ok;
+            more = ahead.ok;
             bool go = true;
             if (more) {
-                const uint32_t st = ua % L::kStages, ph = (ua / L::kStages) & 1;
-                go = warp_wait<kEvery>(bar(K_FULL + st), ph, ctl) && warp_wait<kEvery>(bar(V_FULL + st), ph, ctl);
+                go = warp_wait<kEvery>(bar(K_FULL + ua % L::kStages), (ua / L::kStages) & 1, ctl) &&
+                     warp_wait<kEvery>(bar(V_FULL + ua % L::kStagesV), (ua / L::kStagesV) & 1, ctl);
                 // Q and dO have landed, and the item before has made its last scores (a copy into TMEM is not ordered
                 // behind the products that read the same columns)
                 if (ahead.t == 0) {
@@ -257,18 +262,15 @@ k_cross_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
                     ++items_a;
                 }
                 ++ua;
-                ++made;
-                ahead.next(prm);
             }
             if (use) {
                 // dQ of the item before this one has been read
                 if (cur.t == 0 && items_c++ > 0) go = go && warp_wait<kEvery>(bar(DQ_FREE), items_c & 1, ctl);
                 go = go && warp_wait<kEvery>(bar(DS_FULL + (uc & 1)), (uc >> 1) & 1, ctl);
                 ++uc;
-                --made;
-                cur.next(prm);
             }
             if (!(ok = meet(go))) break;
+            made += (int)more - (int)use;
         }
         if (!ok && lane == 0) { ctl->abort = 1; record_error(prm.err, BSA_EDEVICE, -3); }
     } else if (warp == kPollWarp + 1) {
@@ -308,21 +310,21 @@ k_cross_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
             uint32_t u = 0;
             DqWalk w;
             for (; w.next(prm); ++u) {
-                const int st = u % L::kStages;
-                if (u >= L::kStages && !(ok = mbar_sleep<kEvery>(bar(V_EMPTY + st), (u / L::kStages - 1) & 1, ctl))) break;
+                const int st = u % L::kStagesV;
+                if (u >= L::kStagesV && !(ok = mbar_sleep<kEvery>(bar(V_EMPTY + st), (u / L::kStagesV - 1) & 1, ctl))) break;
                 mbar_expect_tx(bar(V_FULL + st), L::kTileBytes);
                 for (int s = 0; s < D / 64; ++s)
                     tma_load_4d(sbase + L::offV + st * L::kTileBytes + s * L::kSlab, &tmV, s * 64, w.t * kKeys,
                                 (int)prm.G.quot(w.it.h), w.it.b, bar(V_FULL + st));
             }
             if (!ok) { ctl->abort = 1; record_error(prm.err, BSA_EDEVICE, -2); }
-            for (uint32_t st = 0; st < L::kStages; ++st)
-                if (u > st) mbar_drain(bar(V_FULL + st), ((u - 1 - st) / L::kStages) & 1);
+            for (uint32_t st = 0; st < L::kStagesV; ++st)
+                if (u > st) mbar_drain(bar(V_FULL + st), ((u - 1 - st) / L::kStagesV) & 1);
         }
     } else if (warp < kRowWarp) {
         // ------------------------------------------------------------------ softmax
-        const int g = warp / 4, quad = warp & 3;
-        const uint32_t ts = tmem + ((uint32_t)(32 * quad) << 16) + L::colS + g * kKeys, tp = ts - L::colS + L::colDP;
+        const int g = warp / 4, quad = warp & 3;                  // columns [32 g, 32 g + 32) of every tile
+        const uint32_t ts0 = tmem + ((uint32_t)(32 * quad) << 16) + L::colS + g * 32;
         uint32_t u = 0, ni = 0;
         DqItem it;
         for (int k = 0; ok && item_at(prm, k, it); ++k) {
@@ -334,50 +336,36 @@ k_cross_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
             if (lane == 0) mbar_arrive(bar(ROWS_EMPTY + (ni & 1)));
             ++ni;
             for (int t = 0; t < it.nt; ++t, ++u) {
-                if ((int)(u & 1) != g) continue;
+                const uint32_t ts = ts0 + (u & 1) * kKeys, tp = ts - L::colS + L::colDP;
                 uint32_t bits[2];
-                const bool all = prm.keys.bits(it.b, it.len, t * kKeys, lane, bits);
-                if (!(ok = warp_wait<kEvery>(bar(S_FULL + g), (u >> 1) & 1, ctl))) break;
+                prm.keys.bits(it.b, it.len, t * kKeys, lane, bits);
+                const uint32_t word = g ? bits[1] : bits[0];
+                if (!(ok = warp_wait<kEvery>(bar(S_FULL + (u & 1)), (u >> 1) & 1, ctl))) break;
                 fence_after();
-                // 16 columns at a time, the next ones on their way from TMEM
-                uint32_t sv[2][16], dv[2][16];
-                tmem_ld16(ts, sv[0]);
-                tmem_ld16(tp, dv[0]);
-#pragma unroll 1
-                for (int half = 0; half < 2; ++half) {
-                    const uint32_t word = half ? bits[1] : bits[0];
+                uint32_t sv[32], dv[32], pk[16];
+                tmem_ld32(ts, sv);
+                tmem_ld32(tp, dv);
+                tmem_wait_ld();
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const int c = 2 * half + i;
-                        tmem_wait_ld();
-                        if (c < 3) {
-                            tmem_ld16(ts + (c + 1) * 16, sv[i ^ 1]);
-                            tmem_ld16(tp + (c + 1) * 16, dv[i ^ 1]);
-                        }
-                        uint32_t pk[8];
-#pragma unroll
-                        for (int e = 0; e < 16; e += 2) {
-                            float x0, x1, d0, d1;
-                            ffma2(x0, x1, __uint_as_float(sv[i][e]), __uint_as_float(sv[i][e + 1]), prm.scale_log2,
-                                  prm.scale_log2, neg_lse, neg_lse);
-                            fadd2(d0, d1, __uint_as_float(dv[i][e]), __uint_as_float(dv[i][e + 1]), neg_d, neg_d);
-                            const float p0 = ex2_mufu(x0), p1 = ex2_mufu(x1);
-                            fmul2(d0, d1, d0, d1, p0, p1);
-                            pk[e / 2] = pack_bf16(d0, d1);
-                        }
-                        if (!all) {
-                            const uint32_t on = word >> (16 * i);
-#pragma unroll
-                            for (int e = 0; e < 8; ++e)
-                                pk[e] &= (on >> (2 * e) & 1 ? 0xffffu : 0u) | (on >> (2 * e + 1) & 1 ? 0xffff0000u : 0u);
-                        }
-                        tmem_st8(ts + c * 8, pk);
-                    }
+                for (int e = 0; e < 32; e += 2) {
+                    float x0, x1, d0, d1;
+                    ffma2(x0, x1, __uint_as_float(sv[e]), __uint_as_float(sv[e + 1]), prm.scale_log2, prm.scale_log2,
+                          neg_lse, neg_lse);
+                    fadd2(d0, d1, __uint_as_float(dv[e]), __uint_as_float(dv[e + 1]), neg_d, neg_d);
+                    const float p0 = ex2_mufu(x0), p1 = ex2_mufu(x1);
+                    fmul2(d0, d1, d0, d1, p0, p1);
+                    pk[e / 2] = pack_bf16(d0, d1);
                 }
+                if (word != 0xffffffffu) {
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        pk[e] &= (word >> (2 * e) & 1 ? 0xffffu : 0u) | (word >> (2 * e + 1) & 1 ? 0xffff0000u : 0u);
+                }
+                tmem_st16(ts, pk);
                 tmem_wait_st();
                 fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(bar(DS_FULL + g));
+                if (lane == 0) mbar_arrive(bar(DS_FULL + (u & 1)));
             }
         }
         if (!ok) { ctl->abort = 1; record_error(prm.err, BSA_EDEVICE, -4); }
@@ -387,7 +375,7 @@ k_cross_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
         // --------------------------------------------- rows: D ahead of the item, dQ behind it
         const int quad = warp & 3, r = 32 * quad + lane;
         const uint32_t tq = tmem + ((uint32_t)(32 * quad) << 16) + L::colDQ;
-        unsigned char* stage = smem + L::offOut + quad * 4096;
+        unsigned char* stage = smem + L::offOut + quad * L::kOutBytes;
         uint32_t nr = 0, nd = 0, nl = 0;
         // Q and dO of an item, once the copies of the one before have read theirs
         auto load = [&](const DqItem& it) {
@@ -465,8 +453,9 @@ k_cross_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
                 fence_after();
             }
             const int row0 = it.tile * kTile + 32 * quad;
-            uint32_t pk[D / 2];                                       // the row in bf16
-#pragma unroll
+            if (lane == 0) bulk_wait_read();                          // the rows before these have left
+            __syncwarp();
+#pragma unroll 1
             for (int c = 0; c < D / 32; ++c) {
                 uint32_t v[32];
                 if (it.nt > 0) {
@@ -477,26 +466,23 @@ k_cross_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
                     for (int e = 0; e < 32; ++e) v[e] = 0u;
                 }
 #pragma unroll
-                for (int e = 0; e < 16; ++e)
-                    pk[16 * c + e] = pack_bf16(__uint_as_float(v[2 * e]) * prm.scale, __uint_as_float(v[2 * e + 1]) * prm.scale);
+                for (int e = 0; e < 4; ++e) {
+                    uint4 w;
+                    w.x = pack_bf16(__uint_as_float(v[8 * e + 0]) * prm.scale, __uint_as_float(v[8 * e + 1]) * prm.scale);
+                    w.y = pack_bf16(__uint_as_float(v[8 * e + 2]) * prm.scale, __uint_as_float(v[8 * e + 3]) * prm.scale);
+                    w.z = pack_bf16(__uint_as_float(v[8 * e + 4]) * prm.scale, __uint_as_float(v[8 * e + 5]) * prm.scale);
+                    w.w = pack_bf16(__uint_as_float(v[8 * e + 6]) * prm.scale, __uint_as_float(v[8 * e + 7]) * prm.scale);
+                    *reinterpret_cast<uint4*>(stage + swizzled(lane, 4 * c + e, 4096)) = w;
+                }
             }
-            if (it.nt > 0) {                                          // dQ may take the next item
-                fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(DQ_FREE));
-            }
-#pragma unroll
-            for (int s = 0; s < D / 64; ++s) {                        // unrolled: pk stays in registers
-                if (lane == 0) bulk_wait_read();
-                __syncwarp();
-#pragma unroll
-                for (int c = 0; c < 8; ++c)
-                    *reinterpret_cast<uint4*>(stage + swizzled(lane, c, 0)) =
-                        make_uint4(pk[32 * s + 4 * c], pk[32 * s + 4 * c + 1], pk[32 * s + 4 * c + 2], pk[32 * s + 4 * c + 3]);
-                fence_proxy_async();
-                __syncwarp();
-                if (lane == 0 && row0 < prm.N) {
-                    tma_store_4d(&tmDQ, smem_u32(stage), s * 64, row0, it.h, it.b);
+            fence_before();
+            fence_proxy_async();
+            __syncwarp();
+            if (lane == 0) {
+                if (it.nt > 0) mbar_arrive(bar(DQ_FREE));             // dQ may take the next item
+                if (row0 < prm.N) {
+                    for (int s = 0; s < D / 64; ++s)
+                        tma_store_4d(&tmDQ, smem_u32(stage) + s * 4096, s * 64, row0, it.h, it.b);
                     bulk_commit();
                 }
             }
@@ -597,7 +583,7 @@ k_cross_dkv(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUt
     float* row_vals = reinterpret_cast<float*>(smem + L::offRows);
     const uint32_t tmem = begin_cta<kBars>(bar(0), ctl, reinterpret_cast<uint32_t*>(smem + L::offMisc + 16), prm.wait_ns,
                                            [](int i) -> uint32_t {
-                                               return (i >= PD_FULL && i < PD_FULL + 2) || i == ACC_FREE ? 4 : 1;
+                                               return i >= PD_FULL && i < PD_FULL + 2 ? 8 : i == ACC_FREE ? 4 : 1;
                                            });
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
     bool ok = true;
@@ -608,10 +594,13 @@ k_cross_dkv(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUt
                        dq_mn = smem_desc(sbase + L::offQ, L::kSlab, 1024);
         uint32_t ua = 0, uc = 0;
         DkvWalk cur, ahead;
-        cur.next(prm);
-        ahead.next(prm);
-        for (int made = 0; made > 0 || ahead.ok;) {
-            const bool use = made == 2 || !ahead.ok, more = ahead.ok;
+        bool use = true, more = true;
+        for (int made = 0;;) {
+            if (more) ahead.next(prm);
+            if (use) cur.next(prm);
+            if (made == 0 && !ahead.ok) break;
+            use = made == 2 || !ahead.ok;
+            more = ahead.ok;
             if (!(ok = meet(true))) break;
             fence_after();
             if (elect_one()) {
@@ -619,9 +608,9 @@ k_cross_dkv(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUt
                     const uint32_t st = uc % L::kStages, q = st * 2 * L::kTileBytes, buf = (uc & 1) * kKeys;
 #pragma unroll
                     for (int kk = 0; kk < kKeys / 16; ++kk) {
-                        mma_ts(tmem + L::colDV, tmem + L::colS + buf + kk * 8,
+                        mma_ts(tmem + L::colDV, tmem + L::colS + buf + (kk / 2) * 32 + (kk % 2) * 8,
                                desc_at(dq_mn, q + L::kTileBytes + kk * 16 * 128), idesc_g, !cur.first() || kk > 0);
-                        mma_ts(tmem + L::colDK, tmem + L::colDP + buf + kk * 8, desc_at(dq_mn, q + kk * 16 * 128), idesc_g,
+                        mma_ts(tmem + L::colDK, tmem + L::colDP + buf + (kk / 2) * 32 + (kk % 2) * 8, desc_at(dq_mn, q + kk * 16 * 128), idesc_g,
                                !cur.first() || kk > 0);
                     }
                     commit(bar(ST_EMPTY + st));
@@ -641,16 +630,9 @@ k_cross_dkv(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUt
                 }
             }
             __syncwarp();
-            if (use) {
-                ++uc;
-                --made;
-                cur.next(prm);
-            }
-            if (more) {
-                ++ua;
-                ++made;
-                ahead.next(prm);
-            }
+            uc += use;
+            ua += more;
+            made += (int)more - (int)use;
         }
         if (elect_one()) {
             commit(bar(DRAIN));
@@ -660,27 +642,27 @@ k_cross_dkv(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUt
     } else if (warp == kPollWarp) {
         uint32_t ua = 0, uc = 0, items_a = 0, items_c = 0;
         DkvWalk cur, ahead;
-        cur.next(prm);
-        ahead.next(prm);
-        for (int made = 0; made > 0 || ahead.ok;) {
-            const bool use = made == 2 || !ahead.ok, more = ahead.ok;
+        bool use = true, more = true;
+        for (int made = 0;;) {
+            if (more) ahead.next(prm);
+            if (use) cur.next(prm);
+            if (made == 0 && !ahead.ok) break;
+            use = made == 2 || !ahead.ok;
+            more = ahead.ok;
             bool go = true;
             if (more) {
                 go = warp_wait<kEvery>(bar(ST_FULL + ua % L::kStages), (ua / L::kStages) & 1, ctl);
                 if (ahead.first()) go = go && warp_wait<kEvery>(bar(KV_FULL), items_a++ & 1, ctl);
                 ++ua;
-                ++made;
-                ahead.next(prm);
             }
             if (use) {
                 // dK and dV of the item before this one have been read
                 if (cur.first() && items_c++ > 0) go = go && warp_wait<kEvery>(bar(ACC_FREE), items_c & 1, ctl);
                 go = go && warp_wait<kEvery>(bar(PD_FULL + (uc & 1)), (uc >> 1) & 1, ctl);
                 ++uc;
-                --made;
-                cur.next(prm);
             }
             if (!(ok = meet(go))) break;
+            made += (int)more - (int)use;
         }
         if (!ok && lane == 0) { ctl->abort = 1; record_error(prm.err, BSA_EDEVICE, -3); }
     } else if (warp == kPollWarp + 1) {
@@ -736,61 +718,48 @@ k_cross_dkv(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUt
         }
     } else if (warp < kRowWarp) {
         // ------------------------------------------------------------------ softmax
-        const int g = warp / 4, quad = warp & 3;
-        const uint32_t ts = tmem + ((uint32_t)(32 * quad) << 16) + L::colS + g * kKeys, tp = ts - L::colS + L::colDP;
+        const int g = warp / 4, quad = warp & 3;                      // columns [32 g, 32 g + 32) of every tile
+        const uint32_t ts0 = tmem + ((uint32_t)(32 * quad) << 16) + L::colS + g * 32;
         uint32_t u = 0;
         DkvWalk w;
-        while (w.next_item(prm)) {
+        while (ok && w.next_item(prm)) {
             const int j = w.it.kt * kTile + 32 * quad + lane;         // this thread's key
             const bool on = j < w.it.len && (!prm.keys.key_mask || prm.keys.key_mask[(int64_t)w.it.b * prm.keys.M + j]);
             for (int s = w.it.beg; s < w.it.end; ++s, ++u) {
-                if ((int)(u & 1) != g) continue;
                 const int st = u % L::kStages;
+                const uint32_t ts = ts0 + (u & 1) * kKeys, tp = ts - L::colS + L::colDP;
                 if (!(ok = warp_wait<kEvery>(bar(ST_FULL + st), (u / L::kStages) & 1, ctl))) break;
-                if (!(ok = warp_wait<kEvery>(bar(S_FULL + g), (u >> 1) & 1, ctl))) break;
+                if (!(ok = warp_wait<kEvery>(bar(S_FULL + (u & 1)), (u >> 1) & 1, ctl))) break;
                 fence_after();
-                const float* rv = row_vals + st * 2 * kKeys;
-                uint32_t sv[2][16], dv[2][16];
-                tmem_ld16(ts, sv[0]);
-                tmem_ld16(tp, dv[0]);
-#pragma unroll 1
-                for (int half = 0; half < 2; ++half)
+                const float* rv = row_vals + st * 2 * kKeys + g * 32;
+                uint32_t sv[32], dv[32], pk[16], dk[16];
+                tmem_ld32(ts, sv);
+                tmem_ld32(tp, dv);
+                tmem_wait_ld();
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const int c = 2 * half + i;
-                        tmem_wait_ld();
-                        if (c < 3) {
-                            tmem_ld16(ts + (c + 1) * 16, sv[i ^ 1]);
-                            tmem_ld16(tp + (c + 1) * 16, dv[i ^ 1]);
-                        }
-                        uint32_t pk[8], dk[8];
+                for (int e = 0; e < 32; e += 4) {
+                    const float4 l4 = *reinterpret_cast<const float4*>(rv + e);
+                    const float4 d4 = *reinterpret_cast<const float4*>(rv + kKeys + e);
+                    const float l[4] = {l4.x, l4.y, l4.z, l4.w}, d[4] = {d4.x, d4.y, d4.z, d4.w};
 #pragma unroll
-                        for (int e = 0; e < 16; e += 4) {
-                            const float4 l4 = *reinterpret_cast<const float4*>(rv + c * 16 + e);
-                            const float4 d4 = *reinterpret_cast<const float4*>(rv + kKeys + c * 16 + e);
-                            const float l[4] = {l4.x, l4.y, l4.z, l4.w}, d[4] = {d4.x, d4.y, d4.z, d4.w};
-#pragma unroll
-                            for (int f = 0; f < 4; f += 2) {
-                                float x0, x1, d0, d1;
-                                ffma2(x0, x1, __uint_as_float(sv[i][e + f]), __uint_as_float(sv[i][e + f + 1]),
-                                      prm.scale_log2, prm.scale_log2, l[f], l[f + 1]);
-                                fadd2(d0, d1, __uint_as_float(dv[i][e + f]), __uint_as_float(dv[i][e + f + 1]), d[f],
-                                      d[f + 1]);
-                                const float p0 = ex2_mufu(x0), p1 = ex2_mufu(x1);
-                                fmul2(d0, d1, d0, d1, p0, p1);
-                                pk[(e + f) / 2] = on ? pack_bf16(p0, p1) : 0u;
-                                dk[(e + f) / 2] = on ? pack_bf16(d0, d1) : 0u;
-                            }
-                        }
-                        tmem_st8(ts + c * 8, pk);
-                        tmem_st8(tp + c * 8, dk);
+                    for (int f = 0; f < 4; f += 2) {
+                        float x0, x1, d0, d1;
+                        ffma2(x0, x1, __uint_as_float(sv[e + f]), __uint_as_float(sv[e + f + 1]), prm.scale_log2,
+                              prm.scale_log2, l[f], l[f + 1]);
+                        fadd2(d0, d1, __uint_as_float(dv[e + f]), __uint_as_float(dv[e + f + 1]), d[f], d[f + 1]);
+                        const float p0 = ex2_mufu(x0), p1 = ex2_mufu(x1);
+                        fmul2(d0, d1, d0, d1, p0, p1);
+                        pk[(e + f) / 2] = on ? pack_bf16(p0, p1) : 0u;
+                        dk[(e + f) / 2] = on ? pack_bf16(d0, d1) : 0u;
                     }
+                }
+                tmem_st16(ts, pk);
+                tmem_st16(tp, dk);
                 tmem_wait_st();
                 fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(bar(PD_FULL + g));
+                if (lane == 0) mbar_arrive(bar(PD_FULL + (u & 1)));
             }
-            if (!ok) break;
         }
         if (!ok) { ctl->abort = 1; record_error(prm.err, BSA_EDEVICE, -4); }
         tmem_wait_st();
