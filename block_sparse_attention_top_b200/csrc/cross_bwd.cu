@@ -160,8 +160,9 @@ k_cross_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
     using L = DqSmem<D>;
     enum {
         QD_FULL = 0, QD_EMPTY, AB_FREE, S_FULL, DS_FULL = S_FULL + 2, ROWS_FULL = DS_FULL + 2, ROWS_EMPTY = ROWS_FULL + 2,
-        DQ_DONE = ROWS_EMPTY + 2, DQ_FREE, DRAIN, K_RAW, K_FULL, K_EMPTY = K_FULL + L::kStages,
-        V_FULL = K_EMPTY + L::kStages, V_EMPTY = V_FULL + L::kStagesV, kBars = V_EMPTY + L::kStagesV
+        DQ_DONE = ROWS_EMPTY + 2, DQ_FREE, DRAIN, K_FULL, K_EMPTY = K_FULL + L::kStages,
+        V_FULL = K_EMPTY + L::kStages, V_EMPTY = V_FULL + L::kStagesV, K_RAW = V_EMPTY + L::kStagesV,
+        kBars = K_RAW + L::kStages
     };
     static_assert(kBars <= 48, "barrier slots");
     extern __shared__ __align__(1024) unsigned char smem_raw[];
@@ -274,37 +275,22 @@ k_cross_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
         }
         if (!ok && lane == 0) { ctl->abort = 1; record_error(prm.err, BSA_EDEVICE, -3); }
     } else if (warp == kPollWarp + 1) {
-        // K ring.  dQ += dS K: rows of states that do not count become zeros (0 * NaN is NaN)
-        uint32_t u = 0, raw = 0;
-        DqWalk w;
-        for (; w.next(prm); ++u) {
-            const int st = u % L::kStages;
-            if (u >= L::kStages && !(ok = warp_sleep<kEvery>(bar(K_EMPTY + st), (u / L::kStages - 1) & 1, ctl))) break;
-            uint32_t bits[2];
-            const bool all = prm.keys.bits(w.it.b, w.it.len, w.t * kKeys, lane, bits);
-            const bool fix = !all && (prm.keys.key_mask || w.it.len < prm.keys.M);
-            const uint32_t full = bar(fix ? K_RAW : K_FULL + st), dst = sbase + L::offK + st * L::kTileBytes;
-            if (lane == 0) {
-                mbar_expect_tx(full, L::kTileBytes);
-                for (int s = 0; s < D / 64; ++s)
-                    tma_load_4d(dst + s * L::kSlab, &tmK, s * 64, w.t * kKeys, (int)prm.G.quot(w.it.h), w.it.b, full);
-            }
-            if (fix) {
-                if (!warp_wait<kEvery>(full, raw & 1, ctl)) {
-                    mbar_drain(full, raw & 1);
-                    ok = false;
-                    break;
-                }
-                ++raw;
-                zero_rows<D>(smem + (dst - sbase), bits, lane);
-                fence_proxy_async();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(K_FULL + st));
-            }
+        // K ring: dQ += dS K, so rows of states that do not count are zeroed.  S of tile u + 2 is made before tile u is
+        // used up, hence the lag of one.
+        struct {
+            DqWalk w;
+            const DqP& p;
+            __device__ __forceinline__ bool next() { return w.next(p); }
+            __device__ __forceinline__ int b() const { return w.it.b; }
+            __device__ __forceinline__ int head() const { return (int)p.G.quot(w.it.h); }
+            __device__ __forceinline__ int len() const { return w.it.len; }
+            __device__ __forceinline__ int t() const { return w.t; }
+        } walk{DqWalk(), prm};
+        if (!fill_ring<D, L::kStages, 1, kEvery>(walk, prm.keys, &tmK, smem + L::offK, bar(K_FULL), bar(K_EMPTY), bar(K_RAW),
+                                                ctl) && lane == 0) {
+            ctl->abort = 1;
+            record_error(prm.err, BSA_EDEVICE, -1);
         }
-        if (!ok && lane == 0) { ctl->abort = 1; record_error(prm.err, BSA_EDEVICE, -1); }
-        for (uint32_t st = 0; st < L::kStages; ++st)
-            if (u > st) mbar_drain(bar(K_FULL + st), ((u - 1 - st) / L::kStages) & 1);
     } else if (warp == kPollWarp + 2) {
         if (lane == 0) {
             uint32_t u = 0;

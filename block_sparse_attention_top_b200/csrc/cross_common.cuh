@@ -66,11 +66,15 @@ struct Keys {
 template <int D>
 __device__ __forceinline__ void zero_rows(unsigned char* tile, const uint32_t* bits, int lane) {
     constexpr int kLanes = D / 8, kPer = 32 / kLanes;
-    const int c = lane % kLanes;
-#pragma unroll 1
-    for (int i = lane / kLanes; i < kKeys; i += kPer)
-        if (!((i < 32 ? bits[0] : bits[1]) >> (i % 32) & 1))
-            *reinterpret_cast<uint4*>(tile + (c / 8) * kKeys * 128 + i * 128 + (c % 8) * 16) = make_uint4(0, 0, 0, 0);
+    const int c = lane % kLanes, r = lane / kLanes;
+    unsigned char* at = tile + (c / 8) * kKeys * 128 + r * 128 + (c % 8) * 16;
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+        const uint32_t off = ~bits[half] >> r;
+#pragma unroll 8
+        for (int i = 0; i < 32; i += kPer)
+            if (off >> i & 1) *reinterpret_cast<uint4*>(at + (half * 32 + i) * 128) = make_uint4(0, 0, 0, 0);
+    }
 }
 
 // One lane of a converged warp (the same one every time).
@@ -164,6 +168,82 @@ __device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.comm
 // The source of every committed store may be overwritten.
 __device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
 __device__ __forceinline__ void bulk_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+
+// A warp fills a ring of K or V tiles (kKeys rows).  In a tile with states that do not count their rows are
+// overwritten with zeros once the copy has landed (0 * NaN is NaN); kLag (1 or 2) later copies are under way by then.  A
+// tile must be needed only after the stage of the tile kStages - kLag before it has been emptied.  Rows past M are zero
+// already: the copy fills them.  next() moves to the next tile; b(), head(), len(), t() describe it.
+// full, empty, raw: the first of kStages barriers each.  Returns false if a wait ran out.
+template <int D, int kStages, int kLag, uint32_t kEvery, typename Walk>
+__device__ __forceinline__ bool fill_ring(Walk& w, const Keys& keys, const CUtensorMap* map, unsigned char* tiles,
+                                          uint32_t full, uint32_t empty, uint32_t raw, volatile tc::WaitCtl* ctl) {
+    constexpr int kTileBytes = kKeys * D * 2;
+    const int lane = threadIdx.x % 32;
+    struct Fix {
+        bool on = false;
+        int st;
+        uint32_t bits[2];
+    } f1, f0;                                            // of the tile before the last (kLag 2), and the last
+    uint32_t u = 0, phases = 0;                          // bit st: parity of raw[st]
+    int lost = -1;                                       // stage whose copy ran out of time
+    bool ok = true;
+    auto mend = [&](Fix& f) {
+        if (!f.on) return true;
+        const bool landed = tc::warp_wait<kEvery>(raw + 8 * f.st, phases >> f.st & 1, ctl);
+        if (!landed) tc::mbar_drain(raw + 8 * f.st, phases >> f.st & 1);
+        phases ^= 1u << f.st;
+        f.on = false;
+        if (!landed) {
+            lost = f.st;
+            return false;
+        }
+        zero_rows<D>(tiles + f.st * kTileBytes, f.bits, lane);
+        tc::fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(full + 8 * f.st);
+        return true;
+    };
+    bool more = true;
+    for (int after = 0; after < kLag;) {                 // kLag rounds past the last tile
+        if (more) more = w.next();
+        Fix f;
+        if (more) {
+            const int st = u % kStages;
+            if (u >= kStages && !(ok = warp_sleep<kEvery>(empty + 8 * st, (u / kStages - 1) & 1, ctl))) break;
+            const bool all = keys.bits(w.b(), w.len(), w.t() * kKeys, lane, f.bits);
+            f.on = !all && (keys.key_mask || w.len() < keys.M);
+            f.st = st;
+            if (lane == 0) {
+                const uint32_t bar = (f.on ? raw : full) + 8 * st;
+                tc::mbar_expect_tx(bar, kTileBytes);
+                for (int s = 0; s < D / 64; ++s)
+                    tma_load_4d(tc::smem_u32(tiles) + st * kTileBytes + s * kKeys * 128, map, s * 64, w.t() * kKeys, w.head(),
+                                w.b(), bar);
+            }
+            ++u;
+        } else {
+            ++after;
+        }
+        Fix& oldest = kLag == 2 ? f1 : f0;
+        if (!(ok = mend(oldest))) {
+            oldest = f;
+            break;
+        }
+        if (kLag == 2) f1 = f0;
+        f0 = f;
+    }
+    // every copy lands before the CTA exits; stages that were never made full are not waited for
+    if (!ok) {
+        if (f1.on) tc::mbar_drain(raw + 8 * f1.st, phases >> f1.st & 1);
+        if (f0.on) tc::mbar_drain(raw + 8 * f0.st, phases >> f0.st & 1);
+    }
+    for (uint32_t st = 0; st < kStages; ++st) {
+        const bool waits = !ok && ((f1.on && f1.st == (int)st) || (f0.on && f0.st == (int)st) || lost == (int)st);
+        const uint32_t loads = u > st ? (u - 1 - st) / kStages + 1 : 0;
+        if (loads > (uint32_t)waits) tc::mbar_drain(full + 8 * st, (loads - waits - 1) & 1);
+    }
+    return ok;
+}
 
 // bf16 [B, rows, heads, d] with element strides (batch, row, head) as a map of
 // [d, rows, heads, B], box [64, box_rows, 1, 1] with 128-byte swizzle.

@@ -149,10 +149,9 @@ k_cross_fwd(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUt
             const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmO, const FwdP prm) {
     using L = Smem<D>;
     enum {
-        Q_FULL = 0, Q_EMPTY = 2, S_FULL = 4, P_FULL = 8, PV_DONE = 12, O_DONE = 14, O_FREE = 16, DRAIN = 18, V_RAW = 20,
-        K_FULL = 21,
+        Q_FULL = 0, Q_EMPTY = 2, S_FULL = 4, P_FULL = 8, PV_DONE = 12, O_DONE = 14, O_FREE = 16, DRAIN = 18, K_FULL = 20,
         K_EMPTY = K_FULL + L::kStages, V_FULL = K_EMPTY + L::kStages, V_EMPTY = V_FULL + L::kStages,
-        kBars = V_EMPTY + L::kStages
+        V_RAW = V_EMPTY + L::kStages, kBars = V_RAW + L::kStages
     };
     static_assert(kBars <= 40, "barrier slots");
     extern __shared__ __align__(1024) unsigned char smem_raw[];
@@ -171,7 +170,7 @@ k_cross_fwd(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUt
         for (int i = 0; i < kBars; ++i) {
             uint32_t count = 1;
             if ((i >= P_FULL && i < P_FULL + 4) || (i >= O_FREE && i < O_FREE + 2)) count = 4;      // warps
-            if ((i >= K_EMPTY && i < V_FULL) || i >= V_EMPTY) count = 2;                            // MMA threads
+            if ((i >= K_EMPTY && i < V_FULL) || (i >= V_EMPTY && i < V_RAW)) count = 2;    // MMA threads
             mbar_init(bar(i), count);
         }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -226,40 +225,20 @@ k_cross_fwd(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUt
         }
     } else if (warp == kVWarp) {
         // ------------------------------------------------------------------ V ring
-        uint32_t u = 0, raw = 0;
-        bool ok = true;
-        Walk w;
-        for (; w.next(prm); ++u) {
-            const int st = u % L::kStages;
-            if (u >= L::kStages && !(ok = warp_sleep<kEvery>(bar(V_EMPTY + st), (u / L::kStages - 1) & 1, ctl))) break;
-            uint32_t bits[2];
-            const bool all = prm.keys.bits(w.it.b, w.it.len, w.t * kKeys, lane, bits);
-            // rows past M are zero already: the copy fills them
-            const bool fix = !all && (prm.keys.key_mask || w.it.len < prm.keys.M);
-            const uint32_t full = bar(fix ? V_RAW : V_FULL + st);
-            const uint32_t dst = sbase + L::offV + st * L::kTileBytes;
-            if (lane == 0) {
-                mbar_expect_tx(full, L::kTileBytes);
-                for (int s = 0; s < D / 64; ++s)
-                    tma_load_4d(dst + s * L::kSlab, &tmV, s * 64, w.t * kKeys, (int)prm.G.quot(w.it.h), w.it.b, full);
-            }
-            if (fix) {
-                const bool landed = warp_wait<kEvery>(full, raw & 1, ctl);
-                if (!landed) {
-                    mbar_drain(full, raw & 1);
-                    ok = false;
-                    break;
-                }
-                ++raw;
-                zero_rows<D>(smem + (dst - sbase), bits, lane);
-                fence_proxy_async();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(V_FULL + st));
-            }
+        struct {
+            Walk w;
+            const FwdP& p;
+            __device__ __forceinline__ bool next() { return w.next(p); }
+            __device__ __forceinline__ int b() const { return w.it.b; }
+            __device__ __forceinline__ int head() const { return (int)p.G.quot(w.it.h); }
+            __device__ __forceinline__ int len() const { return w.it.len; }
+            __device__ __forceinline__ int t() const { return w.t; }
+        } walk{Walk(), prm};
+        if (!fill_ring<D, L::kStages, 2, kEvery>(walk, prm.keys, &tmV, smem + L::offV, bar(V_FULL), bar(V_EMPTY), bar(V_RAW),
+                                                ctl) && lane == 0) {
+            ctl->abort = 1;
+            record_error(prm.err, BSA_EDEVICE, -2);
         }
-        if (!ok && lane == 0) { ctl->abort = 1; record_error(prm.err, BSA_EDEVICE, -2); }
-        for (uint32_t st = 0; st < L::kStages; ++st)
-            if (u > st) mbar_drain(bar(V_FULL + st), ((u - 1 - st) / L::kStages) & 1);
     } else if (warp == kMmaWarp || warp == kMmaWarp + 1) {
         // -------------------------------------------------------------- MMA issuers
         // The whole warp walks and waits, so that descriptors stay in uniform registers; one lane issues.
