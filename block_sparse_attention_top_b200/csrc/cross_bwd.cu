@@ -286,7 +286,7 @@ k_cross_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
             __device__ __forceinline__ int len() const { return w.it.len; }
             __device__ __forceinline__ int t() const { return w.t; }
         } walk{DqWalk(), prm};
-        if (!fill_ring<D, L::kStages, 1, kEvery>(walk, prm.keys, &tmK, smem + L::offK, bar(K_FULL), bar(K_EMPTY), bar(K_RAW),
+        if (!fill_ring<D, kKeys, L::kStages, 1, kEvery>(walk, prm.keys, &tmK, smem + L::offK, bar(K_FULL), bar(K_EMPTY), bar(K_RAW),
                                                 ctl) && lane == 0) {
             ctl->abort = 1;
             record_error(prm.err, BSA_EDEVICE, -1);

@@ -63,17 +63,17 @@ struct Keys {
 };
 
 // Zeros in the rows of a K or V tile in shared memory whose state does not count (D / 8 lanes to a row).
-template <int D>
+template <int D, int kRows>
 __device__ __forceinline__ void zero_rows(unsigned char* tile, const uint32_t* bits, int lane) {
     constexpr int kLanes = D / 8, kPer = 32 / kLanes;
     const int c = lane % kLanes, r = lane / kLanes;
-    unsigned char* at = tile + (c / 8) * kKeys * 128 + r * 128 + (c % 8) * 16;
+    unsigned char* at = tile + (c / 8) * kRows * 128 + r * 128 + (c % 8) * 16;
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-        const uint32_t off = ~bits[half] >> r;
-#pragma unroll 8
+    for (int w = 0; w < kRows / 32; ++w) {               // (bits stay in registers)
+        const uint32_t off = ~bits[w] >> r;
+#pragma unroll 4
         for (int i = 0; i < 32; i += kPer)
-            if (off >> i & 1) *reinterpret_cast<uint4*>(at + (half * 32 + i) * 128) = make_uint4(0, 0, 0, 0);
+            if (off >> i & 1) *reinterpret_cast<uint4*>(at + (w * 32 + i) * 128) = make_uint4(0, 0, 0, 0);
     }
 }
 
@@ -105,18 +105,19 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* r) {
 // A descriptor `bytes` further on (a multiple of 16, inside the shared memory window).
 __device__ __forceinline__ uint64_t desc_at(uint64_t desc, uint32_t bytes) { return desc + (bytes >> 4); }
 
-// A meeting of two warps (named barrier 1) that tells both whether both are well.  The MMA warp learns this way from
-// a polling warp that its operands are ready: a warp that has issued MMAs stalls on its next shared-memory access
-// until the tensor cores have taken them, and a mbarrier probe is one; the named barrier is not.
-__device__ __forceinline__ bool meet(bool ok) {
+// A meeting of two warps at a named barrier that tells both whether both are well, so that neither waits for one that
+// has given up.  The MMA warp learns this way (barrier 1) from a polling warp that its operands are ready: a warp that
+// has issued MMAs stalls on its next shared-memory access until the tensor cores have taken them, and a mbarrier probe
+// is one; the named barrier is not.
+__device__ __forceinline__ bool meet(bool ok, int id = 1) {
     uint32_t r;
     asm volatile(
         "{\n\t.reg .pred p, q;\n\t"
         "setp.ne.u32 p, %1, 0;\n\t"
-        "bar.red.and.pred q, 1, 64, p;\n\t"
+        "bar.red.and.pred q, %2, 64, p;\n\t"
         "selp.u32 %0, 1, 0, q;\n\t}"
         : "=r"(r)
-        : "r"((uint32_t)ok)
+        : "r"((uint32_t)ok), "r"(id)
         : "memory");
     return r != 0;
 }
@@ -169,20 +170,20 @@ __device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.comm
 __device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
 __device__ __forceinline__ void bulk_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
-// A warp fills a ring of K or V tiles (kKeys rows).  In a tile with states that do not count their rows are
+// A warp fills a ring of K or V tiles (kRows rows).  In a tile with states that do not count their rows are
 // overwritten with zeros once the copy has landed (0 * NaN is NaN); kLag (1 or 2) later copies are under way by then.  A
 // tile must be needed only after the stage of the tile kStages - kLag before it has been emptied.  Rows past M are zero
 // already: the copy fills them.  next() moves to the next tile; b(), head(), len(), t() describe it.
 // full, empty, raw: the first of kStages barriers each.  Returns false if a wait ran out.
-template <int D, int kStages, int kLag, uint32_t kEvery, typename Walk>
+template <int D, int kRows, int kStages, int kLag, uint32_t kEvery, typename Walk>
 __device__ __forceinline__ bool fill_ring(Walk& w, const Keys& keys, const CUtensorMap* map, unsigned char* tiles,
                                           uint32_t full, uint32_t empty, uint32_t raw, volatile tc::WaitCtl* ctl) {
-    constexpr int kTileBytes = kKeys * D * 2;
+    constexpr int kTileBytes = kRows * D * 2;
     const int lane = threadIdx.x % 32;
     struct Fix {
         bool on = false;
         int st;
-        uint32_t bits[2];
+        uint32_t bits[kRows / 32];
     } f1, f0;                                            // of the tile before the last (kLag 2), and the last
     uint32_t u = 0, phases = 0;                          // bit st: parity of raw[st]
     int lost = -1;                                       // stage whose copy ran out of time
@@ -197,7 +198,7 @@ __device__ __forceinline__ bool fill_ring(Walk& w, const Keys& keys, const CUten
             lost = f.st;
             return false;
         }
-        zero_rows<D>(tiles + f.st * kTileBytes, f.bits, lane);
+        zero_rows<D, kRows>(tiles + f.st * kTileBytes, f.bits, lane);
         tc::fence_proxy_async();
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(full + 8 * f.st);
@@ -210,14 +211,17 @@ __device__ __forceinline__ bool fill_ring(Walk& w, const Keys& keys, const CUten
         if (more) {
             const int st = u % kStages;
             if (u >= kStages && !(ok = warp_sleep<kEvery>(empty + 8 * st, (u / kStages - 1) & 1, ctl))) break;
-            const bool all = keys.bits(w.b(), w.len(), w.t() * kKeys, lane, f.bits);
+            bool all = true;
+#pragma unroll
+            for (int i = 0; i < kRows / kKeys; ++i)
+                all &= keys.bits(w.b(), w.len(), w.t() * kRows + i * kKeys, lane, f.bits + 2 * i);
             f.on = !all && (keys.key_mask || w.len() < keys.M);
             f.st = st;
             if (lane == 0) {
                 const uint32_t bar = (f.on ? raw : full) + 8 * st;
                 tc::mbar_expect_tx(bar, kTileBytes);
                 for (int s = 0; s < D / 64; ++s)
-                    tma_load_4d(tc::smem_u32(tiles) + st * kTileBytes + s * kKeys * 128, map, s * 64, w.t() * kKeys, w.head(),
+                    tma_load_4d(tc::smem_u32(tiles) + st * kTileBytes + s * kRows * 128, map, s * 64, w.t() * kRows, w.head(),
                                 w.b(), bar);
             }
             ++u;

@@ -99,44 +99,21 @@ struct Walk {
     }
 };
 
-// 2^x for a pair on the FMA pipe, x >= -126 after clamping: x = j + f with j = rint(x), a degree-4 polynomial for
-// 2^f on [-1/2, 1/2] (our own relative minimax fit, 2.6e-6), j added into the exponent field.
-__device__ __forceinline__ void ex2_fma2(float x0, float x1, float& y0, float& y1) {
-    x0 = fmaxf(x0, -126.f);
-    x1 = fmaxf(x1, -126.f);
-    float t0, t1, j0, j1, f0, f1, p0, p1;
-    fadd2(t0, t1, x0, x1, 12582912.f, 12582912.f);
-    fadd2(j0, j1, t0, t1, -12582912.f, -12582912.f);
-    ffma2(f0, f1, j0, j1, -1.f, -1.f, x0, x1);
-    ffma2(p0, p1, 0.0095701022f, 0.0095701022f, f0, f1, 0.0559178591f, 0.0559178591f);
-    ffma2(p0, p1, p0, p1, f0, f1, 0.2402474433f, 0.2402474433f);
-    ffma2(p0, p1, p0, p1, f0, f1, 0.6931217909f, 0.6931217909f);
-    ffma2(p0, p1, p0, p1, f0, f1, 0.9999992847f, 0.9999992847f);
-    y0 = __int_as_float(__float_as_int(p0) + (__float_as_int(t0) << 23));
-    y1 = __int_as_float(__float_as_int(p1) + (__float_as_int(t1) << 23));
-}
-constexpr int kFmaPairs = 2;         // pairs of every 8 that take the FMA pipe
-
-// 32 scores to 32 probabilities (16 bf16 pairs); adds them to acc.
+// 32 scores to 32 probabilities (16 bf16 pairs); adds them to acc.  (A polynomial on the FMA pipe for an eighth or a
+// quarter of them measured 1 and 4 % slower: MUFU is busy a third of the time.)
 __device__ __forceinline__ void exp_chunk(const uint32_t* x, float scale, float neg_m, float* acc, uint32_t* pk) {
 #pragma unroll
     for (int c = 0; c < 32; c += 2) {
-        float x0, x1, p0, p1;
+        float x0, x1;
         ffma2(x0, x1, __uint_as_float(x[c]), __uint_as_float(x[c + 1]), scale, scale, neg_m, neg_m);
-        if ((c / 2) % 8 >= 8 - kFmaPairs) {
-            ex2_fma2(x0, x1, p0, p1);
-        } else {
-            p0 = ex2_mufu(x0);
-            p1 = ex2_mufu(x1);
-        }
+        const float p0 = ex2_mufu(x0), p1 = ex2_mufu(x1);
         const int u = (c / 2) & 1;
         fadd2(acc[2 * u], acc[2 * u + 1], acc[2 * u], acc[2 * u + 1], p0, p1);
         pk[c / 2] = pack_bf16(p0, p1);
     }
 }
 
-// -inf where a state does not count.  (On the FMA pipe such a score gives 2^-126, not 0: nothing beside a row's sum,
-// and its row of V is zero.)
+// -inf where a state does not count
 __device__ __forceinline__ void mask_cols(uint32_t* s, uint32_t bits) {
 #pragma unroll
     for (int c = 0; c < 32; ++c)
@@ -234,7 +211,7 @@ k_cross_fwd(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUt
             __device__ __forceinline__ int len() const { return w.it.len; }
             __device__ __forceinline__ int t() const { return w.t; }
         } walk{Walk(), prm};
-        if (!fill_ring<D, L::kStages, 2, kEvery>(walk, prm.keys, &tmV, smem + L::offV, bar(V_FULL), bar(V_EMPTY), bar(V_RAW),
+        if (!fill_ring<D, kKeys, L::kStages, 2, kEvery>(walk, prm.keys, &tmV, smem + L::offV, bar(V_FULL), bar(V_EMPTY), bar(V_RAW),
                                                 ctl) && lane == 0) {
             ctl->abort = 1;
             record_error(prm.err, BSA_EDEVICE, -2);
