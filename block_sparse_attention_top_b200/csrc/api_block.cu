@@ -1,5 +1,5 @@
 // C ABI of the block operators: argument validation and launches of the cross
-// attention and of the norms (kernels in cross.cu and norm.cu).
+// attention and of the norms (kernels in cross_*.cu and norm.cu).
 #include "bsa_internal.cuh"
 
 using namespace bsa;
@@ -83,7 +83,7 @@ int bsa_cross_attn(const bsa_plan* p, const void* q, const void* k, const void* 
     if (int rc = cross_args(p, q, k, v, M, Hkv, strides, kv_len, key_mask, &a)) return rc;
     if (!o || misaligned(o, 16) || misaligned(lse, 4) || !on_device(p)) return BSA_EINVAL;
     if (int rc = check_workspace(ws, ws_bytes, cross_ws_bytes(*p, M, Hkv, false))) return rc;
-    return status(launch_cross(*p, a, o, lse, ws, (cudaStream_t)stream));
+    return status(launch_cross(*p, a, o, lse, (cudaStream_t)stream));
 }
 
 int bsa_cross_attn_bwd(const bsa_plan* p, const void* q, const void* k, const void* v, int64_t M, int Hkv,

@@ -122,7 +122,7 @@ struct CrossArgs {
     const uint8_t* key_mask;     // [B, M] or null
 };
 size_t cross_ws_bytes(const bsa_plan& p, int64_t M, int Hkv, bool backward);
-cudaError_t launch_cross(const bsa_plan& p, const CrossArgs& a, void* o, float* lse, void* ws, cudaStream_t s);
+cudaError_t launch_cross(const bsa_plan& p, const CrossArgs& a, void* o, float* lse, cudaStream_t s);
 cudaError_t launch_cross_bwd(const bsa_plan& p, const CrossArgs& a, const void* o, const float* lse, const void* d_o,
                              void* dq, void* dk, void* dv, void* ws, cudaStream_t s);
 struct NormGrads {
