@@ -13,8 +13,7 @@
 //
 // Both passes work in tiles of 64 on the side they walk, with two buffers of
 // S and dP in TMEM.  Each of the softmax warps 0-3 and 4-7 takes half of every
-// tile's columns, a thread per row of the owned side (no sum runs along a row:
-// lse and D are given); P and dS (bf16) overwrite the columns that their
+// tile's columns, a thread per row of the owned side (lse and D are given); P and dS (bf16) overwrite the columns that their
 // thread has read, so the A operand of a product is two runs of 16 columns.
 // The tensor cores make S and dP of tile u+2 behind the products that read
 // tile u.  (Taking turns, each group a whole tile, the softmax of a tile took
@@ -112,7 +111,8 @@ struct DqSmem {
     static constexpr int kOutBytes = 32 * D * 2;
     static constexpr int offOut = offV + kStagesV * kTileBytes;    // 4 warps x 32 rows x D columns
     static constexpr int offRows = offOut + 4 * kOutBytes;         // float lse, D [2 items][128]
-    static constexpr int offBar = offRows + 2 * 2 * kTile * 4;
+    static constexpr int offHalves = offRows + 2 * 2 * kTile * 4;  // float sums of dS [2 items][2 halves][128]
+    static constexpr int offBar = offHalves + 2 * 2 * kTile * 4;
     static constexpr int offMisc = offBar + 48 * 8;
     static constexpr int kAlloc = offMisc + 64 + 1024;
     static constexpr uint32_t colS = 0, colDP = 128, colQ = 256, colDO = 256 + D / 2, colDQ = 384;
@@ -172,6 +172,7 @@ k_cross_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
     auto bar = [&](int i) { return sbase + L::offBar + 8u * (uint32_t)i; };
     volatile WaitCtl* ctl = reinterpret_cast<volatile WaitCtl*>(smem + L::offMisc);
     float* row_vals = reinterpret_cast<float*>(smem + L::offRows);
+    float* halves = reinterpret_cast<float*>(smem + L::offHalves);
     const uint32_t tmem = begin_cta<kBars>(bar(0), ctl, reinterpret_cast<uint32_t*>(smem + L::offMisc + 16), prm.wait_ns,
                                            [](int i) -> uint32_t {
                                                if ((i >= DS_FULL && i < DS_FULL + 2) || (i >= ROWS_EMPTY && i < ROWS_EMPTY + 2)) return 8;
@@ -180,6 +181,7 @@ k_cross_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
                                            });
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
     bool ok = true;
+    auto wait_full = [&](uint32_t b, uint32_t parity) { return warp_wait<kEvery>(b, parity, ctl); };
 
     if (warp == kMmaWarp) {
         constexpr uint32_t idesc_s = instr_desc(kKeys, 0), idesc_dq = instr_desc(D, 1);
@@ -313,46 +315,82 @@ k_cross_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
         const uint32_t ts0 = tmem + ((uint32_t)(32 * quad) << 16) + L::colS + g * 32;
         uint32_t u = 0, ni = 0;
         DqItem it;
+        // Both warps of a row leave together: one that has given up says so at the other's next exchange, and every
+        // item has exactly one.
+        auto give_up = [&] {
+            meet(false, 2 + quad);
+            ok = false;
+        };
         for (int k = 0; ok && item_at(prm, k, it); ++k) {
             if (it.nt == 0) continue;
-            if (!(ok = warp_wait<kEvery>(bar(ROWS_FULL + (ni & 1)), (ni >> 1) & 1, ctl))) break;
+            if (!wait_full(bar(ROWS_FULL + (ni & 1)), (ni >> 1) & 1)) {
+                give_up();
+                break;
+            }
             const float* rv = row_vals + (ni & 1) * 2 * kTile + 32 * quad + lane;
-            const float neg_lse = -rv[0], neg_d = -rv[kTile];
+            const float neg_lse = -rv[0];
+            float neg_d = -rv[kTile], sum = 0.f;                      // sum: of this half's dS so far
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(ROWS_EMPTY + (ni & 1)));
+            float* mine = halves + ((ni & 1) * 2 + g) * kTile + 32 * quad + lane;
+            const float* theirs = halves + ((ni & 1) * 2 + 1 - g) * kTile + 32 * quad + lane;
             ++ni;
-            for (int t = 0; t < it.nt; ++t, ++u) {
+            // D from the rounded o is off by what dS sums to over all states (0 for the exact D)
+            auto correct = [&] {
+                *mine = sum;
+                if (!meet(true, 2 + quad)) return false;
+                neg_d -= sum + *theirs;
+                return true;
+            };
+            for (int t = 0; t < it.nt && ok; ++t, ++u) {
                 const uint32_t ts = ts0 + (u & 1) * kKeys, tp = ts - L::colS + L::colDP;
                 uint32_t bits[2];
                 prm.keys.bits(it.b, it.len, t * kKeys, lane, bits);
                 const uint32_t word = g ? bits[1] : bits[0];
-                if (!(ok = warp_wait<kEvery>(bar(S_FULL + (u & 1)), (u >> 1) & 1, ctl))) break;
+                if (!wait_full(bar(S_FULL + (u & 1)), (u >> 1) & 1)) {
+                    give_up();
+                    break;
+                }
                 fence_after();
                 uint32_t sv[32], dv[32], pk[16];
                 tmem_ld32(ts, sv);
                 tmem_ld32(tp, dv);
                 tmem_wait_ld();
+                if (word != 0xffffffffu) {                            // P = 0, dS = 0
 #pragma unroll
-                for (int e = 0; e < 32; e += 2) {
-                    float x0, x1, d0, d1;
-                    ffma2(x0, x1, __uint_as_float(sv[e]), __uint_as_float(sv[e + 1]), prm.scale_log2, prm.scale_log2,
-                          neg_lse, neg_lse);
-                    fadd2(d0, d1, __uint_as_float(dv[e]), __uint_as_float(dv[e + 1]), neg_d, neg_d);
-                    const float p0 = ex2_mufu(x0), p1 = ex2_mufu(x1);
-                    fmul2(d0, d1, d0, d1, p0, p1);
-                    pk[e / 2] = pack_bf16(d0, d1);
+                    for (int e = 0; e < 32; ++e) {
+                        sv[e] = word >> e & 1 ? sv[e] : __float_as_uint(-INFINITY);
+                        dv[e] = word >> e & 1 ? dv[e] : 0u;
+                    }
                 }
-                if (word != 0xffffffffu) {
+                // one tile holds all states: its dS with the corrected D
+#pragma unroll 1
+                for (int pass = it.nt == 1 ? 0 : 1; pass < 2; ++pass) {
+                    float acc[4] = {};
 #pragma unroll
-                    for (int e = 0; e < 16; ++e)
-                        pk[e] &= (word >> (2 * e) & 1 ? 0xffffu : 0u) | (word >> (2 * e + 1) & 1 ? 0xffff0000u : 0u);
+                    for (int e = 0; e < 32; e += 2) {
+                        float x0, x1, d0, d1;
+                        ffma2(x0, x1, __uint_as_float(sv[e]), __uint_as_float(sv[e + 1]), prm.scale_log2, prm.scale_log2,
+                              neg_lse, neg_lse);
+                        fadd2(d0, d1, __uint_as_float(dv[e]), __uint_as_float(dv[e + 1]), neg_d, neg_d);
+                        const float p0 = ex2_mufu(x0), p1 = ex2_mufu(x1);
+                        fmul2(d0, d1, d0, d1, p0, p1);
+                        fadd2(acc[e & 2], acc[(e & 2) + 1], acc[e & 2], acc[(e & 2) + 1], d0, d1);
+                        pk[e / 2] = pack_bf16(d0, d1);
+                    }
+                    sum += (acc[0] + acc[1]) + (acc[2] + acc[3]);
+                    if (pass == 0 && !(ok = correct())) break;
                 }
+                if (!ok) break;
                 tmem_st16(ts, pk);
                 tmem_wait_st();
                 fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(DS_FULL + (u & 1)));
             }
+            if (!ok || (it.nt > 1 && !(ok = correct()))) break;
+            const int n = it.tile * kTile + 32 * quad + lane;
+            if (g == 0 && n < prm.N) prm.dsum[((int64_t)it.b * prm.H + it.h) * prm.N + n] = -neg_d;
         }
         if (!ok) { ctl->abort = 1; record_error(prm.err, BSA_EDEVICE, -4); }
         tmem_wait_st();
@@ -416,7 +454,6 @@ k_cross_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
                 const int64_t i = ((int64_t)it.b * prm.H + it.h) * prm.N + n;
                 const float l = prm.lse[i];
                 lse2 = l == -INFINITY ? 0.f : l * kLog2e;             // no valid state: every key is masked
-                prm.dsum[i] = d;
             }
             float* rv = row_vals + (nr & 1) * 2 * kTile + r;
             rv[0] = lse2;

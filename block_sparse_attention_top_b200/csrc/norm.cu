@@ -767,6 +767,7 @@ NormP norm_params(const bsa_plan& p, const bsa_norm_args& a) {
 int row_threads(int C) { return ((C + kCols - 1) / kCols + 31) / 32 * 32; }
 
 constexpr int kSmemPerSm = 227 * 1024, kRegsPerSm = 65536;
+constexpr int kPlainSmem = 40 * 1024;    // dynamic bytes that need no opt-in: 48 KB less what the kernels hold statically
 // CTAs of `threads` with `regs` registers a thread and `smem` bytes that an SM holds.
 int ctas_per_sm(int threads, int regs, int smem) {
     return std::max(1, std::min({2048 / threads, 32, kRegsPerSm / (threads * regs), kSmemPerSm / (smem + 2048)}));
@@ -803,7 +804,7 @@ cudaError_t fwd(const bsa_plan& p, const NormP& n, const void* x, const void* y,
     const int smem = VEC == 8 ? (three ? 3 : 2) * row_bytes : 0;
     auto kern = threads <= 320 ? (three || VEC == 1 ? k_norm_cta<TX, VEC, 3, 320> : k_norm_cta<TX, VEC, 2, 320>)
                                : (three || VEC == 1 ? k_norm_cta<TX, VEC, 3, 1024> : k_norm_cta<TX, VEC, 2, 1024>);
-    if (smem > 48 * 1024)
+    if (smem > kPlainSmem)
         if (cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) return e;
     const Ranges rg{n.rows, (int)std::min<int64_t>(n.rows, (int64_t)p.num_sms * ctas_per_sm(threads, threads <= 320 ? 102 : 64, smem))};
     kern<<<rg.n, threads, smem, s>>>(n, rg, xi, yi, (TX*)x_out, (__nv_bfloat16*)h);
@@ -824,7 +825,7 @@ template <typename TX, int VEC, int NC, int kThreads, bool kToken, bool kPost, b
 cudaError_t bwd_t(const BwdCall& b) {
     auto kern = k_norm_bwd<TX, VEC, NC, kThreads, kToken, kPost, kRing>;
     const int smem = kRing ? kBwdStages * b.stage : 0;
-    if (smem > 48 * 1024)
+    if (smem > kPlainSmem)
         if (cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) return e;
     kern<<<b.rg.n, b.threads, smem, b.s>>>(b.n, b.g, b.rg, (const __nv_bfloat16*)b.dh, (const TX*)b.dx_out,
                                            (const TX*)b.x_out, (const __nv_bfloat16*)b.y, (TX*)b.dx, (__nv_bfloat16*)b.dy);
