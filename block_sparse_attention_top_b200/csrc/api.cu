@@ -128,16 +128,21 @@ int bsa_plan_create(bsa_plan** out, int B, int H, int T, int Hs, int Ws,
 
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return BSA_ECUDA;
-    cudaDeviceProp prop;
-    if (cudaGetDeviceProperties(&prop, dev) != cudaSuccess) return BSA_ECUDA;
-    if (prop.major != 10 || prop.minor != 0) return BSA_EUNSUPPORTED;
+    // four attributes: filling the whole cudaDeviceProp takes most of a millisecond
+    int major = 0, minor = 0, sms = 0, l2 = 0;
+    if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&l2, cudaDevAttrL2CacheSize, dev) != cudaSuccess)
+        return BSA_ECUDA;
+    if (major != 10 || minor != 0) return BSA_EUNSUPPORTED;
 
     bsa_plan* p = new (std::nothrow) bsa_plan();
     if (!p) return BSA_ECUDA;
     p->B = B; p->H = H; p->T = T; p->Hs = Hs; p->Ws = Ws; p->d = head_dim; p->block = block;
     p->order = order; p->N = N; p->nb = nb; p->rows = (int64_t)B * H * nb;
-    p->device = dev; p->num_sms = prop.multiProcessorCount;
-    p->l2_bytes = prop.l2CacheSize; p->schedule = BSA_SCHED_L2_HEADS;
+    p->device = dev; p->num_sms = sms;
+    p->l2_bytes = l2; p->schedule = BSA_SCHED_L2_HEADS;
     p->wait_ns = 4000000000ull;
     std::vector<int32_t> perm((size_t)N);
     token_order(T, Hs, Ws, order, perm.data());

@@ -703,6 +703,7 @@ k_norm_bwd_join(const NormP p, const GradP g, const Ranges rg, int64_t groups) {
     auto join = [&](const float* src, int64_t stride, int first, int count, float* out) {
         float s[3] = {0.f, 0.f, 0.f};
         if (c < p.C)
+#pragma unroll 4
             for (int i = threadIdx.y; i < count; i += kShares) {
                 // a split group's pieces: slot 1 of the CTA it begins in, slot 0 of the others
                 const float* q = src + (first + i) * stride + (stride == 6 * (int64_t)p.C && i == 0 ? 3 * (int64_t)p.C : 0) + c;
