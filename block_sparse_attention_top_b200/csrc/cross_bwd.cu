@@ -35,13 +35,6 @@ constexpr int kThreads = 16 * 32;
 constexpr uint32_t kTmemCols = 512;
 constexpr float kLog2e = 1.4426950408889634f;
 
-__device__ __forceinline__ void fmul2(float& d0, float& d1, float a0, float a1, float b0, float b1) {
-    asm("{\n\t.reg .b64 ra, rb, rd;\n\t"
-        "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
-        "mul.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
-        : "=f"(d0), "=f"(d1)
-        : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
-}
 // Address of 16-byte chunk c of row r in a tile of 64-column slabs with 128-byte swizzle.
 __device__ __forceinline__ uint32_t swizzled(int r, int c, int slab_bytes) {
     return (uint32_t)((c / 8) * slab_bytes + r * 128 + (((c % 8) ^ (r & 7)) * 16));

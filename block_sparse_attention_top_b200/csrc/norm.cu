@@ -27,6 +27,7 @@
 #include <cuda_bf16.h>
 
 #include "bsa_internal.cuh"
+#include "tc_common.cuh"
 
 namespace bsa {
 namespace {
@@ -487,10 +488,29 @@ k_norm_bwd(const NormP p, const GradP g, const Ranges rg, const __nv_bfloat16* d
         for (int k = 0; k < R; ++k)
             if (c.in(k)) store_cols<VEC>(t + c.at(k), v + k * VEC);
     };
+    // The arithmetic of a row is in pairs of channels (f32x2): it issues half as many instructions, which bound the
+    // kernel (72 % of issue slots at 5120 channels with single ones).
+    auto pairs = [&](auto f) {
+#pragma unroll
+        for (int i = 0; i < NC; i += 2) f(i);
+    };
     auto total = [&](const float* v) {
-        float s = 0.f;
-        each([&](int i) { s += v[i]; });
-        return s;
+        float s0 = 0.f, s1 = 0.f;
+        pairs([&](int i) { tc::fadd2(s0, s1, s0, s1, v[i], v[i + 1]); });
+        return s0 + s1;
+    };
+    auto centred = [&](float* v, float mean) {
+#pragma unroll
+        for (int k = 0; k < R; ++k) {
+            if constexpr (VEC == 8) {
+                if (c.in(k))                             // channels past C hold 0
+#pragma unroll
+                    for (int e = 0; e < 8; e += 2)
+                        tc::fadd2(v[8 * k + e], v[8 * k + e + 1], v[8 * k + e], v[8 * k + e + 1], -mean, -mean);
+            } else {
+                v[k] = c.in(k) ? v[k] - mean : 0.f;
+            }
+        }
     };
 
     // kToken: dweight, dbias, dpost_weight sums of the CTA; else A, S, T of the current group
@@ -541,18 +561,18 @@ k_norm_bwd(const NormP p, const GradP g, const Ranges rg, const __nv_bfloat16* d
         if (dh) {
             get(x_out + base, st, 0, xh);
             get(dh + base, st, off_h, gh);
-            if (lx) {
-#pragma unroll
-                for (int k = 0; k < R; ++k)
-#pragma unroll
-                    for (int e = 0; e < VEC; ++e) xh[k * VEC + e] = c.in(k) ? xh[k * VEC + e] - mean_x : 0.f;
-            }
-            each([&](int i) {
-                const float gr = gh[i] * ca[i];
-                sums[0] += xh[i] * xh[i];
-                sums[1] += gr;
-                sums[2] += gr * xh[i];
+            if (lx) centred(xh, mean_x);
+            float q0 = 0.f, q1 = 0.f, s0 = 0.f, s1 = 0.f, x0 = 0.f, x1 = 0.f;
+            pairs([&](int i) {
+                float g0, g1;
+                tc::fmul2(g0, g1, gh[i], gh[i + 1], ca[i], ca[i + 1]);
+                tc::ffma2(q0, q1, xh[i], xh[i + 1], xh[i], xh[i + 1], q0, q1);
+                tc::fadd2(s0, s1, s0, s1, g0, g1);
+                tc::ffma2(x0, x1, g0, g1, xh[i], xh[i + 1], x0, x1);
             });
+            sums[0] = q0 + q1;
+            sums[1] = s0 + s1;
+            sums[2] = x0 + x1;
             if (lx && row + 1 < r1) {
                 get(x_out + base + p.C, nx, 0, d);
                 sums[3] = total(d);
@@ -560,13 +580,10 @@ k_norm_bwd(const NormP p, const GradP g, const Ranges rg, const __nv_bfloat16* d
         }
         if (y) get(y + base, st, off_y, yh);
         if constexpr (kPost) {
-            if (ly) {
-#pragma unroll
-                for (int k = 0; k < R; ++k)
-#pragma unroll
-                    for (int e = 0; e < VEC; ++e) yh[k * VEC + e] = c.in(k) ? yh[k * VEC + e] - mean_y : 0.f;
-            }
-            each([&](int i) { sums[4] += yh[i] * yh[i]; });
+            if (ly) centred(yh, mean_y);
+            float q0 = 0.f, q1 = 0.f;
+            pairs([&](int i) { tc::ffma2(q0, q1, yh[i], yh[i + 1], yh[i], yh[i + 1], q0, q1); });
+            sums[4] = q0 + q1;
             if (ly && row + 1 < r1) {
                 get(y + base + p.C, nx, off_y, d);
                 sums[5] = total(d);
@@ -581,9 +598,12 @@ k_norm_bwd(const NormP p, const GradP g, const Ranges rg, const __nv_bfloat16* d
         if (dh) {
             const float rx = rsqrtf(sums[0] * p.inv_c + p.eps);
             const float m0 = p.norm == BSA_NORM_LAYER ? sums[1] * p.inv_c : 0.f, m1 = sums[2] * rx * p.inv_c;
-            each([&](int i) {
-                xh[i] *= rx;
-                d[i] += rx * (gh[i] * ca[i] - m0 - xh[i] * m1);
+            pairs([&](int i) {
+                float t0, t1;
+                tc::fmul2(xh[i], xh[i + 1], xh[i], xh[i + 1], rx, rx);
+                tc::ffma2(t0, t1, gh[i], gh[i + 1], ca[i], ca[i + 1], -m0, -m0);
+                tc::ffma2(t0, t1, xh[i], xh[i + 1], -m1, -m1, t0, t1);
+                tc::ffma2(d[i], d[i + 1], rx, rx, t0, t1, d[i], d[i + 1]);
             });
             if constexpr (kToken) {
                 if (g.dshift) store(g.dshift + gbase, gh);
@@ -597,16 +617,16 @@ k_norm_bwd(const NormP p, const GradP g, const Ranges rg, const __nv_bfloat16* d
                 }
                 if (p.scale) param(gh, p.scale + gbase, times1);
             }
-            each([&](int i) {
-                sa[i] += gh[i] * xh[i];
-                ss[i] += gh[i];
+            pairs([&](int i) {
+                tc::ffma2(sa[i], sa[i + 1], gh[i], gh[i + 1], xh[i], xh[i + 1], sa[i], sa[i + 1]);
+                tc::fadd2(ss[i], ss[i + 1], ss[i], ss[i + 1], gh[i], gh[i + 1]);
             });
         }
         if (y) {
             float ry = 1.f;
             if constexpr (kPost) {
                 ry = rsqrtf(sums[4] * p.inv_c + p.eps);
-                each([&](int i) { yh[i] *= ry; });
+                pairs([&](int i) { tc::fmul2(yh[i], yh[i + 1], yh[i], yh[i + 1], ry, ry); });
             }
             if constexpr (kToken) {
                 float t[NC];
@@ -620,7 +640,7 @@ k_norm_bwd(const NormP p, const GradP g, const Ranges rg, const __nv_bfloat16* d
                 if (p.gate) param(t, p.gate + gbase, times);
                 each([&](int i) { st_[i] += t[i] * yh[i]; });
             } else {
-                each([&](int i) { st_[i] += d[i] * yh[i]; });
+                pairs([&](int i) { tc::ffma2(st_[i], st_[i + 1], d[i], d[i + 1], yh[i], yh[i + 1], st_[i], st_[i + 1]); });
             }
             if constexpr (kPost) {
                 // channels past C: cg is 1 there, yh 0
@@ -637,10 +657,11 @@ k_norm_bwd(const NormP p, const GradP g, const Ranges rg, const __nv_bfloat16* d
                 const float m0 = p.post == BSA_NORM_LAYER ? two[0] * p.inv_c : 0.f, m1 = two[1] * p.inv_c;
                 each([&](int i) { yh[i] = ry * (d[i] * cg[i] - m0 - yh[i] * m1); });
             } else {
-                each([&](int i) { yh[i] = d[i] * cg[i]; });
+                pairs([&](int i) { tc::fmul2(yh[i], yh[i + 1], d[i], d[i + 1], cg[i], cg[i + 1]); });
             }
             store(dy + base, yh);
-            each([&](int i) { d[i] *= p.res_scale; });
+            if (p.res_scale != 1.f)
+                pairs([&](int i) { tc::fmul2(d[i], d[i + 1], d[i], d[i + 1], p.res_scale, p.res_scale); });
         }
         store(dx + base, d);
         st = nx;
