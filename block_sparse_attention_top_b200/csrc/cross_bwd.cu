@@ -13,11 +13,24 @@
 //
 // Both passes work in tiles of 64 on the side they walk, with two buffers of
 // S and dP in TMEM.  Each of the softmax warps 0-3 and 4-7 takes half of every
-// tile's columns, a thread per row of the owned side (lse and D are given); P and dS (bf16) overwrite the columns that their
-// thread has read, so the A operand of a product is two runs of 16 columns.
+// tile's columns, a thread per row of the owned side (lse and D are given);
+// P and dS (bf16) overwrite the columns that their thread has read, so the A
+// operand of a product is two runs of 16 columns.
 // The tensor cores make S and dP of tile u+2 behind the products that read
 // tile u.  (Taking turns, each group a whole tile, the softmax of a tile took
 // 1500 cycles, longer than the tensor cores' 1400 for the tile between.)
+//
+// D comes from the bf16 O, off by up to 2^-8 of the terms it sums; where a few
+// states hold nearly all of P that error is as large as dP - D itself.  For
+// the exact D a row of dS sums to 0, so the sum that is left is the error:
+// k_cross_dq takes it out of its own dS where all states fit one tile, and
+// always out of the D that k_cross_dkv reads.
+//
+// Bound by the softmax warps' and the tensor cores' taking turns on a tile.
+// Measured with 32 760 tokens, 12 heads of 128, 512 states: k_cross_dq 185 us,
+// k_cross_dkv 200, the sum of shares 8 (five products at a GEMM's rate:
+// 156 us).  Both kernels were held back by their code first: at 120 KB the
+// instruction caches were busy 87 % of the time, at 33 KB 2 %.
 //
 // Waits are bounded as in attn_pp.cu.
 #include <algorithm>
@@ -127,7 +140,7 @@ __device__ __forceinline__ bool item_at(const DqP& p, int k, DqItem& it) {
 }
 struct DqWalk {
     DqItem it;
-    int k = -1, t = 0;
+    int k = -1, t = 0, nth = -1;     // nth: which of the items with keys
     bool ok = true;
     __device__ __forceinline__ DqWalk() { it.nt = 0; }
     __device__ __forceinline__ bool next(const DqP& p) {
@@ -140,6 +153,7 @@ struct DqWalk {
             ++k;
             ok = item_at(p, k, it);
         } while (ok && it.nt == 0);
+        ++nth;
         return ok;
     }
     __device__ __forceinline__ bool last() const { return t == it.nt - 1; }
@@ -181,14 +195,16 @@ k_cross_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
         const uint64_t dk = smem_desc(sbase + L::offK, 16, 1024), dv = smem_desc(sbase + L::offV, 16, 1024),
                        dk_mn = smem_desc(sbase + L::offK, L::kSlab, 1024), dqd = smem_desc(sbase + L::offQ, 16, 1024);
         uint32_t ua = 0, uc = 0;                                  // steps: scores made, dQ added
-        DqWalk cur, ahead;                                        // ahead: the step whose scores are made next
+        // ahead: the step whose scores are made next, at most in the item after cur's: an item's Q and dO come while the
+        // one before it is added up, so the second item after cur's waits for cur's dQ
+        DqWalk cur, ahead;
         bool use = true, more = true;
         for (int made = 0;;) {                                    // scores made and not yet used
             if (more) ahead.next(prm);
             if (use) cur.next(prm);
             if (made == 0 && !ahead.ok) break;
             use = made == 2 || !ahead.ok;
-            more = ahead.ok;
+            more = ahead.ok && ahead.nth - cur.nth < 2;
             if (!(ok = meet(true))) break;
             fence_after();
             if (elect_one()) {
@@ -245,7 +261,7 @@ k_cross_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
             if (use) cur.next(prm);
             if (made == 0 && !ahead.ok) break;
             use = made == 2 || !ahead.ok;
-            more = ahead.ok;
+            more = ahead.ok && ahead.nth - cur.nth < 2;
             bool go = true;
             if (more) {
                 go = warp_wait<kEvery>(bar(K_FULL + ua % L::kStages), (ua / L::kStages) & 1, ctl) &&

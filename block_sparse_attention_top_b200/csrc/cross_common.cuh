@@ -1,5 +1,6 @@
 // Shared by the cross-attention kernels: parameters, valid-state masks, 4-D
-// tensor maps over [B, rows, heads, d] tensors and their TMA copies.
+// tensor maps over [B, rows, heads, d] tensors and their TMA copies.  (The norms
+// take fmul2 from here.)
 #pragma once
 
 #include <cuda_bf16.h>
@@ -86,6 +87,15 @@ __device__ __forceinline__ bool elect_one() {
         "selp.u32 %0, 1, 0, p;\n\t}"
         : "=r"(p));
     return p != 0;
+}
+
+// Packed fp32 pairs beside tc::ffma2 and tc::fadd2: d = a * b.
+__device__ __forceinline__ void fmul2(float& d0, float& d1, float a0, float a1, float b0, float b1) {
+    asm("{\n\t.reg .b64 ra, rb, rd;\n\t"
+        "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
+        "mul.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+        : "=f"(d0), "=f"(d1)
+        : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
 }
 
 // A descriptor `bytes` further on (a multiple of 16, inside the shared memory window).

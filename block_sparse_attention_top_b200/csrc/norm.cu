@@ -27,7 +27,7 @@
 #include <cuda_bf16.h>
 
 #include "bsa_internal.cuh"
-#include "tc_common.cuh"
+#include "cross_common.cuh"
 
 namespace bsa {
 namespace {
@@ -565,7 +565,7 @@ k_norm_bwd(const NormP p, const GradP g, const Ranges rg, const __nv_bfloat16* d
             float q0 = 0.f, q1 = 0.f, s0 = 0.f, s1 = 0.f, x0 = 0.f, x1 = 0.f;
             pairs([&](int i) {
                 float g0, g1;
-                tc::fmul2(g0, g1, gh[i], gh[i + 1], ca[i], ca[i + 1]);
+                cross::fmul2(g0, g1, gh[i], gh[i + 1], ca[i], ca[i + 1]);
                 tc::ffma2(q0, q1, xh[i], xh[i + 1], xh[i], xh[i + 1], q0, q1);
                 tc::fadd2(s0, s1, s0, s1, g0, g1);
                 tc::ffma2(x0, x1, g0, g1, xh[i], xh[i + 1], x0, x1);
@@ -600,7 +600,7 @@ k_norm_bwd(const NormP p, const GradP g, const Ranges rg, const __nv_bfloat16* d
             const float m0 = p.norm == BSA_NORM_LAYER ? sums[1] * p.inv_c : 0.f, m1 = sums[2] * rx * p.inv_c;
             pairs([&](int i) {
                 float t0, t1;
-                tc::fmul2(xh[i], xh[i + 1], xh[i], xh[i + 1], rx, rx);
+                cross::fmul2(xh[i], xh[i + 1], xh[i], xh[i + 1], rx, rx);
                 tc::ffma2(t0, t1, gh[i], gh[i + 1], ca[i], ca[i + 1], -m0, -m0);
                 tc::ffma2(t0, t1, xh[i], xh[i + 1], -m1, -m1, t0, t1);
                 tc::ffma2(d[i], d[i + 1], rx, rx, t0, t1, d[i], d[i + 1]);
@@ -626,7 +626,7 @@ k_norm_bwd(const NormP p, const GradP g, const Ranges rg, const __nv_bfloat16* d
             float ry = 1.f;
             if constexpr (kPost) {
                 ry = rsqrtf(sums[4] * p.inv_c + p.eps);
-                pairs([&](int i) { tc::fmul2(yh[i], yh[i + 1], yh[i], yh[i + 1], ry, ry); });
+                pairs([&](int i) { cross::fmul2(yh[i], yh[i + 1], yh[i], yh[i + 1], ry, ry); });
             }
             if constexpr (kToken) {
                 float t[NC];
@@ -657,11 +657,11 @@ k_norm_bwd(const NormP p, const GradP g, const Ranges rg, const __nv_bfloat16* d
                 const float m0 = p.post == BSA_NORM_LAYER ? two[0] * p.inv_c : 0.f, m1 = two[1] * p.inv_c;
                 each([&](int i) { yh[i] = ry * (d[i] * cg[i] - m0 - yh[i] * m1); });
             } else {
-                pairs([&](int i) { tc::fmul2(yh[i], yh[i + 1], d[i], d[i + 1], cg[i], cg[i + 1]); });
+                pairs([&](int i) { cross::fmul2(yh[i], yh[i + 1], d[i], d[i + 1], cg[i], cg[i + 1]); });
             }
             store(dy + base, yh);
             if (p.res_scale != 1.f)
-                pairs([&](int i) { tc::fmul2(d[i], d[i + 1], d[i], d[i + 1], p.res_scale, p.res_scale); });
+                pairs([&](int i) { cross::fmul2(d[i], d[i + 1], d[i], d[i + 1], p.res_scale, p.res_scale); });
         }
         store(dx + base, d);
         st = nx;
