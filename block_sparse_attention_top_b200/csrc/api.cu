@@ -1,7 +1,8 @@
 // libbsa C ABI: plans, argument validation, workspace layout, stream-ordered
 // launch sequences.  Kernels live in route.cu, route_static.cu, masks.cu,
 // augment.cu, prepare.cu, attn_pp.cu (block 128), attn_tc.cu (block 64) and
-// attn_simt.cu; balance.cu is host code.
+// attn_simt.cu; balance.cu is host code.  The operators of a block around its
+// self-attention have their entry points in api_block.cu.
 #include <algorithm>
 #include <cmath>
 #include <cstring>

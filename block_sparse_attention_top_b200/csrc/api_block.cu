@@ -21,6 +21,7 @@ int check_workspace(const void* ws, size_t bytes, size_t need) {
 
 bool overlaps_null(int64_t extent, const void* p) { return extent > 0 && !p; }
 
+constexpr int64_t kMaxStates = 1ll << 30;
 constexpr int64_t kMaxStride = 1ll << 39;     // in elements: a tensor map's strides are below 2^40 bytes
 
 // Extents [B, rows, heads] with their strides: dense defaults filled in, limits checked.
@@ -40,7 +41,7 @@ int cross_args(const bsa_plan* p, const void* q, const void* k, const void* v, i
     if (!p || !q || M < 0 || Hkv < 1 || overlaps_null(M, k) || overlaps_null(M, v)) return BSA_EINVAL;
     if (p->H % Hkv != 0) return BSA_EINVAL;
     if (misaligned(q, 16) || misaligned(k, 16) || misaligned(v, 16) || misaligned(kv_len, 4)) return BSA_EINVAL;
-    if (M > (1ll << 30) || (int64_t)p->B * p->H * p->N > INT32_MAX || (int64_t)p->B * M * Hkv > INT32_MAX)
+    if (M > kMaxStates || (int64_t)p->B * p->H * p->N > INT32_MAX || (int64_t)p->B * M * Hkv > INT32_MAX)
         return BSA_EUNSUPPORTED;
     a->q = q; a->k = k; a->v = v; a->M = M; a->Hkv = Hkv;
     a->kv_len = kv_len; a->key_mask = key_mask;
@@ -65,6 +66,14 @@ int norm_args(const bsa_plan* p, const bsa_norm_args* a) {
     return BSA_OK;
 }
 
+// The gradients of the parameters leave in 16-byte stores where the width allows.
+bool misaligned(const NormGrads& g) {
+    const void* out[6] = {g.dgate, g.dscale, g.dshift, g.dweight, g.dbias, g.dpost_weight};
+    for (const void* q : out)
+        if (misaligned(q, 16)) return true;
+    return false;
+}
+
 int status(cudaError_t e) { return e == cudaSuccess ? BSA_OK : BSA_ECUDA; }
 
 }  // namespace
@@ -72,7 +81,7 @@ int status(cudaError_t e) { return e == cudaSuccess ? BSA_OK : BSA_ECUDA; }
 extern "C" {
 
 size_t bsa_cross_attn_workspace_size(const bsa_plan* p, int64_t M, int Hkv, int backward) {
-    if (!p || M < 0 || Hkv < 1 || p->H % Hkv != 0) return 0;
+    if (!p || M < 0 || M > kMaxStates || Hkv < 1 || p->H % Hkv != 0) return 0;
     return cross_ws_bytes(*p, M, Hkv, backward != 0);
 }
 
@@ -125,11 +134,10 @@ int bsa_norm_modulate_bwd(const bsa_plan* p, const bsa_norm_args* a, const void*
                           void* stream) {
     if (int rc = norm_args(p, a)) return rc;
     if (!dh || !x || !dx || a->norm == BSA_NORM_NONE || a->post_norm != BSA_NORM_NONE) return BSA_EINVAL;
-    if (misaligned(dh, 16) || misaligned(x, 16) || misaligned(dx, 16) || misaligned(dscale, 4) ||
-        misaligned(dshift, 4) || misaligned(dweight, 4) || misaligned(dbias, 4) || !on_device(p))
+    const NormGrads g{nullptr, dscale, dshift, dweight, dbias, nullptr};
+    if (misaligned(dh, 16) || misaligned(x, 16) || misaligned(dx, 16) || misaligned(g) || !on_device(p))
         return BSA_EINVAL;
     if (int rc = check_workspace(ws, ws_bytes, norm_bwd_ws_bytes(*p, *a))) return rc;
-    const NormGrads g{nullptr, dscale, dshift, dweight, dbias, nullptr};
     return status(launch_norm_bwd(*p, *a, g, dh, nullptr, x, nullptr, dx, nullptr, ws, (cudaStream_t)stream));
 }
 
@@ -140,13 +148,11 @@ int bsa_residual_norm_bwd(const bsa_plan* p, const bsa_norm_args* a, const void*
     if (int rc = norm_args(p, a)) return rc;
     if (!y || !dx || !dy || (!dh && !dx_out) || (dh != nullptr) != (a->norm != BSA_NORM_NONE) || (dh && !x_out))
         return BSA_EINVAL;
+    const NormGrads g{dgate, dscale, dshift, dweight, dbias, dpost_weight};
     if (misaligned(dh, 16) || misaligned(dx_out, 16) || misaligned(x_out, 16) || misaligned(y, 16) ||
-        misaligned(dx, 16) || misaligned(dy, 16) || misaligned(dgate, 4) || misaligned(dscale, 4) ||
-        misaligned(dshift, 4) || misaligned(dweight, 4) || misaligned(dbias, 4) || misaligned(dpost_weight, 4) ||
-        !on_device(p))
+        misaligned(dx, 16) || misaligned(dy, 16) || misaligned(g) || !on_device(p))
         return BSA_EINVAL;
     if (int rc = check_workspace(ws, ws_bytes, norm_bwd_ws_bytes(*p, *a))) return rc;
-    const NormGrads g{dgate, dscale, dshift, dweight, dbias, dpost_weight};
     return status(launch_norm_bwd(*p, *a, g, dh, dx_out, x_out, y, dx, dy, ws, (cudaStream_t)stream));
 }
 

@@ -15,7 +15,10 @@
  *     3.4) read as an e4m3 P.V product;
  *   - around them: the SASA augmentation (section 3 "Stage 3", Eqs. 7-10),
  *     the runtime load-balancing planner (section 3 "Stage 2", Eqs. 1-6) and
- *     a window + rotating-anchor mask producer (the LVSA wiki page).
+ *     a window + rotating-anchor mask producer (the LVSA wiki page);
+ *   - not on the pages: the rest of a transformer block next to the
+ *     self-attention, cross attention to an encoder's states and the norms
+ *     at the block's boundaries, forward and backward.
  *
  * Conventions shared by every call
  *   - Q, K, V, O: [B, N, H, d] row-major (d fastest), N = T*Hs*Ws tokens in
@@ -445,6 +448,7 @@ int bsa_attn_run_simt(const bsa_plan* plan, const int32_t* row_ptr, const int32_
  * self-attention they stand next to (its B, N, H, head_dim, device, error
  * word and wait limit; its block size and token order play no part, raster
  * order in and out).  The plan's device must be current (BSA_EINVAL).
+ * Device arrays are 16-byte aligned; kv_len and lse 4, key_mask 1.
  * ------------------------------------------------------------------------
  */
 
@@ -483,8 +487,10 @@ int bsa_cross_attn(const bsa_plan* plan, const void* q, const void* k, const voi
  * head.  q, k, v, M, Hkv, strides, kv_len, key_mask: as in the forward call;
  * o, lse: its outputs; d_o: bf16 [B,N,H,d] dense.  dq [B,N,H,d], dk, dv
  * [B,M,Hkv,d]: bf16, dense; states that do not count get zero gradients, and
- * so do query rows without a valid state.  P and dS enter the products in
- * bf16, sums are fp32, and the result does not depend on scheduling: the
+ * so do query rows without a valid state.  D comes from the bf16 O; what its
+ * rounding makes dS sum to over the states (0 for the exact D) is taken out
+ * again, for dK always and for dQ where M <= 64.  P and dS enter the products
+ * in bf16, sums are fp32, and the result does not depend on scheduling: the
  * same inputs give the same bits.
  * workspace: >= bsa_cross_attn_workspace_size(plan, M, Hkv, 1) bytes, 256-aligned.
  */

@@ -14,6 +14,8 @@ Modules:
   stripes    periodic diagonal stripe block masks (six parameters per head)
   sasa       slack-aware augmentation budget (Eqs. 7-10) and the augmented CSR
   rlb        runtime load balancing: rank loads, rho, the pair-swap plan search
+  block      cross attention and the norms at a block's boundaries, forward and
+             backward, with bounds on their rounding errors
 
 Pin status: every function is pinned by tests/test_oracle_*.py against
 closed forms, invariants, brute force or a library routine (see each module's

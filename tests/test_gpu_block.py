@@ -450,6 +450,52 @@ def test_norm_refusals_with_a_plan(bsa):
     assert e.value.status == bsa.BSA_EWORKSPACE
 
 
+@pytest.mark.parametrize("M,kind", [(13, "mask"), (64, "all"), (1, "all"), (100, "len")])
+def test_many_items_of_few_states(bsa, M, kind):
+    """Several items to every SM, each with one or two key tiles: what an item leaves for the output warps (its rows'
+    sums and maxima) stays until they have read it, however far the softmax warps run ahead."""
+    B, N, H, Hkv, d = 2, 6216, 9, 3, 128
+    sharp = torch.logspace(-2, 1, H, base=2).to(torch.bfloat16).cuda().view(1, 1, H, 1)
+    q, do = rand((B, N, H, d), 71) * sharp, rand((B, N, H, d), 72)
+    k, v = rand((B, M, Hkv, d), 73), rand((B, M, Hkv, d), 74)
+    kv_len, key_mask = masks_of(kind, B, M, 5)
+    on = ob.valid_states(B, M, kv_len, key_mask)
+    kw = dict(kv_len=None if kv_len is None else torch.from_numpy(kv_len.astype(np.int32)).cuda(),
+              key_mask=None if key_mask is None else torch.from_numpy(key_mask).cuda())
+    plan = plan_of(bsa, B, N, H, d)
+    o, lse = bsa.cross_attn(plan, q, k, v, return_lse=True, **kw)
+    check_cross(o, lse, q, k, v, on)
+    grads = bsa.cross_attn_backward(plan, do, q, k, v, o, lse, **kw)
+    for _ in range(20):
+        o2, lse2 = bsa.cross_attn(plan, q, k, v, return_lse=True, **kw)
+        assert torch.equal(o, o2) and torch.equal(lse, lse2)
+        for a, b in zip(grads, bsa.cross_attn_backward(plan, do, q, k, v, o, lse, **kw)):
+            assert torch.equal(a, b)
+    assert bsa.bsa_last_device_error(plan) == bsa.BSA_OK
+
+
+@pytest.mark.parametrize("which", ["dgate", "dscale", "dshift", "dweight", "dbias", "dpost_weight"])
+@pytest.mark.parametrize("off", [4, 8])
+def test_norm_gradients_refuse_outputs_off_the_16_byte_grid(bsa, which, off):
+    """The C call takes any device pointers: what 16-byte stores could not write is refused before the launch."""
+    import ctypes
+    plan, x, t, kw, opt, store, F = norm_case(bsa, 1, 2, 5, 64, "token", "f32", "layer", None, ALL)
+    lib, y = bsa._lib, t["y"]
+    names = ["dgate", "dscale", "dshift", "dweight", "dbias", "dpost_weight"]
+    out = {n: torch.empty(10 * 64 + 4, device="cuda") for n in names}
+    ptr = {n: o.data_ptr() + (off if n == which else 0) for n, o in out.items()}
+    ws = torch.empty(1 << 22, dtype=torch.uint8, device="cuda")
+    dx, dy = torch.empty_like(x), torch.empty_like(y)
+    a = bsa.NormArgs(64, 10, bsa.BSA_F32, bsa.BSA_NORM_LAYER, bsa.BSA_NORM_NONE, 1e-6, 1.0)
+    rc = lib.bsa_residual_norm_bwd(plan.handle, ctypes.byref(a), y.data_ptr(), x.data_ptr(), x.data_ptr(), y.data_ptr(),
+                                   dx.data_ptr(), dy.data_ptr(), *(ptr[n] for n in names), ws.data_ptr(), ws.numel(), 0)
+    assert rc == bsa.BSA_EINVAL
+    if which in names[1:5]:
+        rc = lib.bsa_norm_modulate_bwd(plan.handle, ctypes.byref(a), y.data_ptr(), x.data_ptr(), dx.data_ptr(),
+                                       *(ptr[n] for n in names[1:5]), ws.data_ptr(), ws.numel(), 0)
+        assert rc == bsa.BSA_EINVAL
+
+
 # -------------------------------------------------------- streams, graphs, a whole block
 
 def test_gradients_are_the_same_every_time(bsa):
