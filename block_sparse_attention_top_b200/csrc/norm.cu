@@ -141,6 +141,15 @@ __device__ __forceinline__ void fetch_commit() { asm volatile("cp.async.commit_g
 template <int n>
 __device__ __forceinline__ void fetch_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(n) : "memory"); }
 
+// Rows off the 16-byte grid do not come through a ring: their 128-byte lines are brought to L2 two rows ahead, a line to a
+// thread (1219 channels, sandwich: 250 -> 241 us; in the backward kernel it cost 3 %).  (A
+// thread holds at most 64 bytes of the row.)
+template <typename T>
+__device__ __forceinline__ void prefetch_row(const T* p, int C) {
+    if (threadIdx.x * 128 < C * sizeof(T))
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(reinterpret_cast<const char*>(p) + threadIdx.x * 128));
+}
+
 // A thread's slots of one row of type T in a ring stage: 16-byte pieces, piece i at [i][thread].
 template <typename T>
 constexpr int row_pieces() { return kCols * (int)sizeof(T) / 16; }
@@ -326,6 +335,9 @@ k_norm_cta(const NormP p, const Ranges rg, const TX* x, const __nv_bfloat16* y, 
                 if (y) fetch_row(ring + st * stage + x_bytes, y + row * p.C, c);
             }
             fetch_commit();
+        } else if (row < r1) {
+            prefetch_row(x + row * p.C, p.C);
+            if (y) prefetch_row(y + row * p.C, p.C);
         }
     };
     for (int i = 0; i < kStages - 1; ++i) fetch(r0 + i, i);
@@ -333,6 +345,7 @@ k_norm_cta(const NormP p, const Ranges rg, const TX* x, const __nv_bfloat16* y, 
     int64_t grp = r0 / p.group_rows, left = 0;           // rows of the group still to come
     for (int64_t row = r0; row < r1; ++row) {
         const int n = (int)(row - r0);
+        float v[kCols], u[kCols];
         if (left == 0) {
             grp = row / p.group_rows;
             left = (grp + 1) * p.group_rows - row;
@@ -340,7 +353,6 @@ k_norm_cta(const NormP p, const Ranges rg, const TX* x, const __nv_bfloat16* y, 
         }
         --left;
         fetch(row + kStages - 1, (n + kStages - 1) % kStages);
-        float v[kCols], u[kCols];
         if constexpr (VEC == 8) {
             fetch_wait<kStages - 1>();
             const unsigned char* s = ring + n % kStages * stage;
@@ -820,15 +832,24 @@ cudaError_t fwd(const bsa_plan& p, const NormP& n, const void* x, const void* y,
         return cudaGetLastError();
     }
     const int threads = row_threads(n.C);
-    // a ring of three rows, of two where three would leave an SM with one CTA
+    // A ring of three rows, of two where three would leave an SM with one CTA (320 threads, 5120 channels) or not fit.
     const int row_bytes = threads * kCols * (int)(sizeof(TX) + (y ? 2 : 0));
-    const bool three = 3 * row_bytes <= 96 * 1024;
+    const bool three = 3 * row_bytes <= (threads <= 320 ? 96 : 200) * 1024;
     const int smem = VEC == 8 ? (three ? 3 : 2) * row_bytes : 0;
-    auto kern = threads <= 320 ? (three || VEC == 1 ? k_norm_cta<TX, VEC, 3, 320> : k_norm_cta<TX, VEC, 2, 320>)
-                               : (three || VEC == 1 ? k_norm_cta<TX, VEC, 3, 1024> : k_norm_cta<TX, VEC, 2, 1024>);
+    // Up to 640 threads a CTA to an SM with 96 registers a thread is faster than two with 64, which spill (6144 channels
+    // 572 against 654 us); not for scalar loads, which need the warps (5308 channels 2.77 against 2.03 ms).
+    const bool roomy = VEC == 8 && threads <= 640;
+    auto kern = k_norm_cta<TX, VEC, 3, 1024>;
+    if constexpr (VEC == 8) {
+        if (threads <= 320) kern = three ? k_norm_cta<TX, VEC, 3, 320> : k_norm_cta<TX, VEC, 2, 320>;
+        else if (roomy) kern = k_norm_cta<TX, VEC, 3, 640>;
+        else if (!three) kern = k_norm_cta<TX, VEC, 2, 1024>;
+    } else if (threads <= 320) {
+        kern = k_norm_cta<TX, VEC, 3, 320>;
+    }
     if (smem > kPlainSmem)
         if (cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) return e;
-    const Ranges rg{n.rows, (int)std::min<int64_t>(n.rows, (int64_t)p.num_sms * ctas_per_sm(threads, threads <= 320 ? 102 : 64, smem))};
+    const Ranges rg{n.rows, (int)std::min<int64_t>(n.rows, (int64_t)p.num_sms * ctas_per_sm(threads, threads <= 320 || roomy ? 102 : 64, smem))};
     kern<<<rg.n, threads, smem, s>>>(n, rg, xi, yi, (TX*)x_out, (__nv_bfloat16*)h);
     return cudaGetLastError();
 }
