@@ -921,6 +921,11 @@ cudaError_t launch_norm_bwd(const bsa_plan& p, const bsa_norm_args& a, const Nor
     const BwdCall b{n, g, rg, dh, dx_out, x_out, y, dx, dy, bwd_threads(a.C), bwd_stage_bytes(a), s};
     cudaError_t e = a.dtype == BSA_BF16 ? bwd<__nv_bfloat16>(b) : bwd<float>(b);
     if (e != cudaSuccess) return e;
+    // No h: its scale and shift have no part in the result.  The kernel writes a token's own gradients where it has a dh;
+    // those of larger groups come out of its sums, which are 0.
+    if (!dh && n.group_rows == 1)
+        for (float* d : {g.dscale, g.dshift})
+            if (d && (e = cudaMemsetAsync(d, 0, (size_t)n.rows * n.C * sizeof(float), s)) != cudaSuccess) return e;
     const int64_t groups = n.group_rows == 1 ? 0 : n.rows / n.group_rows;
     k_norm_bwd_join<<<dim3((n.C + 31) / 32, 1 + (unsigned)std::min<int64_t>(groups, 1024)), dim3(32, kShares), 0, s>>>(
         n, g, rg, groups);

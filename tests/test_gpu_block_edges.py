@@ -1,0 +1,58 @@
+"""Calls of the block operators at the edges of what their documentation allows, on the GPU."""
+import ctypes
+
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def bsa():
+    from block_sparse_attention_top_b200 import build
+    build.build()
+    import block_sparse_attention_top_b200 as m
+    return m
+
+
+def rand(shape, seed, dtype=torch.bfloat16, scale=1.0):
+    g = torch.Generator().manual_seed(seed)
+    return (torch.randn(*shape, generator=g) * scale).to(dtype).cuda()
+
+
+def plan_of(bsa, B, N, H, d):
+    return bsa.Plan(B, H, 1, 1, N, d, 64, bsa.BSA_ORDER_IDENTITY)
+
+
+# ------------------------------------------------------------------------ the norms
+
+@pytest.mark.parametrize("stream", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("C", [8, 129, 520, 1219, 5120, 8200])
+@pytest.mark.parametrize("N,groups", [(6, 6), (1, 1), (6, 2), (6, 1)])
+def test_gradients_of_parameters_that_make_no_h_are_zero(bsa, N, groups, C, stream):
+    """norm NONE: the boundary makes no h, so scale, shift, weight and bias have no part in it.  Every gradient that is
+    asked for is written all the same: zeros."""
+    B = 2
+    plan = plan_of(bsa, B, N, 1, 64)
+    x, y, dxo = rand((B, N, C), 1, stream), rand((B, N, C), 2), rand((B, N, C), 3, stream)
+    par = {n: rand(s, 4 + i, torch.float32) for i, (n, s) in enumerate(
+        dict(gate=(B, groups, C), scale=(B, groups, C), shift=(B, groups, C), weight=(C,), bias=(C,),
+             post_weight=(C,)).items())}
+    a = bsa.NormArgs(C, groups, bsa.BSA_BF16 if stream == torch.bfloat16 else bsa.BSA_F32, bsa.BSA_NORM_NONE,
+                     bsa.BSA_NORM_RMS, 1e-6, 1.0, *(par[n].data_ptr() for n in
+                                                    ("gate", "scale", "shift", "weight", "bias", "post_weight")))
+    names = ("gate", "scale", "shift", "weight", "bias", "post_weight")
+    out = {n: torch.full_like(par[n], float("nan")) for n in names}
+    dx, dy = torch.full_like(x, float("nan")), torch.full_like(y, float("nan"))
+    ws = torch.empty(bsa._lib.bsa_norm_bwd_workspace_size(plan.handle, ctypes.byref(a)), dtype=torch.uint8, device="cuda")
+    rc = bsa._lib.bsa_residual_norm_bwd(plan.handle, ctypes.byref(a), None, dxo.data_ptr(), x.data_ptr(), y.data_ptr(),
+                                        dx.data_ptr(), dy.data_ptr(), *(out[n].data_ptr() for n in names),
+                                        ws.data_ptr(), ws.numel(), torch.cuda.current_stream().cuda_stream)
+    assert rc == bsa.BSA_OK
+    torch.cuda.synchronize()
+    for n in ("scale", "shift", "weight", "bias"):
+        assert (out[n] == 0).all(), n
+    plain = bsa.residual_norm_backward(plan, None, dxo, x, y, gate=par["gate"], post_weight=par["post_weight"],
+                                       norm=bsa.BSA_NORM_NONE, post_norm=bsa.BSA_NORM_RMS)
+    for got, want in ((dx, plain.dx), (dy, plain.dy), (out["gate"], plain.dgate), (out["post_weight"], plain.dpost_weight)):
+        assert torch.equal(got, want)
