@@ -781,7 +781,9 @@ k_norm_bwd_join(const NormP p, const GradP g, const Ranges rg, int64_t groups) {
     }
 }
 
-NormP norm_params(const bsa_plan& p, const bsa_norm_args& a) {
+// Parameters that have no part in a call are null from here on, whatever the caller's struct holds there: gate and
+// post_weight without a branch y, the affine and the modulation without an h.
+NormP norm_params(const bsa_plan& p, const bsa_norm_args& a, bool has_y) {
     NormP n;
     n.C = a.C;
     n.rows = (int64_t)p.B * p.N;
@@ -792,8 +794,13 @@ NormP norm_params(const bsa_plan& p, const bsa_norm_args& a) {
     n.res_scale = a.res_scale;
     n.c = (float)a.C;
     n.inv_c = 1.f / n.c;
-    n.gate = a.gate; n.scale = a.scale; n.shift = a.shift;
-    n.weight = a.weight; n.bias = a.bias; n.post_weight = a.post_weight;
+    const bool has_h = a.norm != BSA_NORM_NONE;
+    n.gate = has_y ? a.gate : nullptr;
+    n.post_weight = has_y ? a.post_weight : nullptr;
+    n.scale = has_h ? a.scale : nullptr;
+    n.shift = has_h ? a.shift : nullptr;
+    n.weight = has_h ? a.weight : nullptr;
+    n.bias = has_h ? a.bias : nullptr;
     return n;
 }
 
@@ -897,7 +904,7 @@ cudaError_t bwd(const BwdCall& b) {
 
 cudaError_t launch_norm(const bsa_plan& p, const bsa_norm_args& a, const void* x, const void* y, void* x_out, void* h,
                         cudaStream_t s) {
-    const NormP n = norm_params(p, a);
+    const NormP n = norm_params(p, a, y != nullptr);
     const bool wide = a.C % 8 == 0;
     if (a.dtype == BSA_BF16)
         return wide ? fwd<__nv_bfloat16, 8>(p, n, x, y, x_out, h, s) : fwd<__nv_bfloat16, 1>(p, n, x, y, x_out, h, s);
@@ -911,7 +918,7 @@ size_t norm_bwd_ws_bytes(const bsa_plan& p, const bsa_norm_args& a) {
 cudaError_t launch_norm_bwd(const bsa_plan& p, const bsa_norm_args& a, const NormGrads& out, const void* dh,
                             const void* dx_out, const void* x_out, const void* y, void* dx, void* dy, void* ws,
                             cudaStream_t s) {
-    const NormP n = norm_params(p, a);
+    const NormP n = norm_params(p, a, y != nullptr);
     const Ranges rg{n.rows, bwd_ctas(p, a)};
     GradP g;
     g.dgate = out.dgate; g.dscale = out.dscale; g.dshift = out.dshift;

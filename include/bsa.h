@@ -527,8 +527,9 @@ typedef struct bsa_norm_args {
 
 /*
  * h = (norm(x) * weight + bias) * (1 + scale) + shift, rows of C channels.
- * x: [B,N,C] of args->dtype; h: bf16 [B,N,C].  gate, post_weight and
- * res_scale are not read; post_norm must be BSA_NORM_NONE and norm not.
+ * x: [B,N,C] of args->dtype; h: bf16 [B,N,C].  The arrays at gate and
+ * post_weight, and res_scale, are not read, here and in the gradient;
+ * post_norm must be BSA_NORM_NONE and norm not.
  */
 int bsa_norm_modulate(const bsa_plan* plan, const bsa_norm_args* args, const void* x, void* h, void* stream);
 
@@ -537,8 +538,9 @@ int bsa_norm_modulate(const bsa_plan* plan, const bsa_norm_args* args, const voi
  *   x_out = res_scale * x + gate * (post_norm(y) * post_weight),
  *   h     = (norm(x_out) * weight + bias) * (1 + scale) + shift.
  * x, x_out: [B,N,C] of args->dtype; y, h: bf16 [B,N,C].  h is NULL exactly
- * when args->norm is BSA_NORM_NONE.  h is taken from the fp32 sum, before
- * x_out is rounded.  x_out may be x and h may be y; no other overlap.
+ * when args->norm is BSA_NORM_NONE; the arrays at scale, shift, weight and
+ * bias are not read then, here and in the gradient, and their gradients are
+ * zero.  h is taken from the fp32 sum, before x_out is rounded.  x_out may be x and h may be y; no other overlap.
  */
 int bsa_residual_norm(const bsa_plan* plan, const bsa_norm_args* args, const void* x, const void* y, void* x_out,
                       void* h, void* stream);

@@ -38,6 +38,7 @@ def test_gradients_of_parameters_that_make_no_h_are_zero(bsa, N, groups, C, stre
     par = {n: rand(s, 4 + i, torch.float32) for i, (n, s) in enumerate(
         dict(gate=(B, groups, C), scale=(B, groups, C), shift=(B, groups, C), weight=(C,), bias=(C,),
              post_weight=(C,)).items())}
+    par["scale"][0, 0, 0], par["weight"][0] = float("inf"), float("nan")   # not read: they make no h
     a = bsa.NormArgs(C, groups, bsa.BSA_BF16 if stream == torch.bfloat16 else bsa.BSA_F32, bsa.BSA_NORM_NONE,
                      bsa.BSA_NORM_RMS, 1e-6, 1.0, *(par[n].data_ptr() for n in
                                                     ("gate", "scale", "shift", "weight", "bias", "post_weight")))
@@ -56,3 +57,31 @@ def test_gradients_of_parameters_that_make_no_h_are_zero(bsa, N, groups, C, stre
                                        norm=bsa.BSA_NORM_NONE, post_norm=bsa.BSA_NORM_RMS)
     for got, want in ((dx, plain.dx), (dy, plain.dy), (out["gate"], plain.dgate), (out["post_weight"], plain.dpost_weight)):
         assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("C", [24, 129, 1536])
+@pytest.mark.parametrize("groups", [1, 2, 6])
+def test_norm_modulate_reads_no_gate_and_no_post_weight(bsa, groups, C):
+    """One struct of arguments for both norm operators: what norm_modulate and its gradient do not read may hold
+    anything (here NaN, one group of it)."""
+    B, N = 2, 6
+    plan = plan_of(bsa, B, N, 1, 64)
+    x, dh = rand((B, N, C), 1, torch.float32), rand((B, N, C), 2)
+    par = dict(scale=rand((B, groups, C), 3, torch.float32), shift=rand((B, groups, C), 4, torch.float32),
+               weight=rand((C,), 5, torch.float32), bias=rand((C,), 6, torch.float32))
+    h, grads = bsa.norm_modulate(plan, x, **par), bsa.norm_modulate_backward(plan, dh, x, **par)
+    nan = torch.full((B * N * C,), float("nan"), device="cuda")
+    p = {n: t.data_ptr() for n, t in par.items()}
+    a = bsa.NormArgs(C, groups, bsa.BSA_F32, bsa.BSA_NORM_LAYER, bsa.BSA_NORM_NONE, 1e-6, float("nan"), nan.data_ptr(),
+                     p["scale"], p["shift"], p["weight"], p["bias"], nan.data_ptr())
+    s = torch.cuda.current_stream().cuda_stream
+    h2, dx = torch.empty_like(h), torch.empty_like(x)
+    assert bsa._lib.bsa_norm_modulate(plan.handle, ctypes.byref(a), x.data_ptr(), h2.data_ptr(), s) == bsa.BSA_OK
+    out = {n: torch.empty_like(t) for n, t in par.items()}
+    ws = torch.empty(bsa._lib.bsa_norm_bwd_workspace_size(plan.handle, ctypes.byref(a)), dtype=torch.uint8, device="cuda")
+    assert bsa._lib.bsa_norm_modulate_bwd(plan.handle, ctypes.byref(a), dh.data_ptr(), x.data_ptr(), dx.data_ptr(),
+                                          *(out[n].data_ptr() for n in par), ws.data_ptr(), ws.numel(), s) == bsa.BSA_OK
+    torch.cuda.synchronize()
+    assert torch.equal(h, h2) and torch.equal(dx, grads.dx)
+    for n in par:
+        assert torch.equal(out[n], getattr(grads, "d" + n)), n
