@@ -48,6 +48,16 @@ __device__ __forceinline__ void record_error(int32_t* err, int status, int detai
     if (atomicCAS(err, 0, status) == 0) err[1] = detail;
 }
 
+// Before a launch of `kern` with `smem` dynamic bytes.  What a kernel may use is a property of the kernel on the device,
+// not of the call: it is set to the same `most` every time, the largest that any call needs, never to this call's own
+// size, which another host thread could lower between this and the launch.  (40 KB: with what a kernel holds
+// statically below the 48 KB that need no consent.)
+template <typename K>
+cudaError_t allow_smem(K kern, size_t smem, size_t most) {
+    if (smem <= 40 * 1024) return cudaSuccess;
+    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
+}
+
 // ---- launchers (return cudaError_t of the launch) ----
 // The routing stages of bsa_route / bsa_route_static (pool, scores, row
 // routing) into the given scratch on `s`; the CSR stage follows.

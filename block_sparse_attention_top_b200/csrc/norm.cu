@@ -808,14 +808,16 @@ NormP norm_params(const bsa_plan& p, const bsa_norm_args& a, bool has_y) {
 int row_threads(int C) { return ((C + kCols - 1) / kCols + 31) / 32 * 32; }
 
 constexpr int kSmemPerSm = 227 * 1024, kRegsPerSm = 65536;
-constexpr int kPlainSmem = 40 * 1024;    // dynamic bytes that need no opt-in: 48 KB less what the kernels hold statically
+constexpr int kRingBytes = 200 * 1024;   // the largest ring of any variant
+template <typename K>
+cudaError_t allow_ring(K kern, int smem) { return allow_smem(kern, smem, kRingBytes); }
+
 // CTAs of `threads` with `regs` registers a thread and `smem` bytes that an SM holds.
 int ctas_per_sm(int threads, int regs, int smem) {
     return std::max(1, std::min({2048 / threads, 32, kRegsPerSm / (threads * regs), kSmemPerSm / (smem + 2048)}));
 }
 
 // The gradient's CTAs (its workspace depends on them): as many as fit, 8 rows at least to each.
-constexpr int kRingBytes = 200 * 1024;
 int bwd_threads(int C) { return ((C + bwd_cols(C) - 1) / bwd_cols(C) + 31) / 32 * 32; }
 // bytes of a ring stage, 0: no ring (rows off the 16-byte grid, or too long)
 int bwd_stage_bytes(const bsa_norm_args& a) {
@@ -841,7 +843,7 @@ cudaError_t fwd(const bsa_plan& p, const NormP& n, const void* x, const void* y,
     const int threads = row_threads(n.C);
     // A ring of three rows, of two where three would leave an SM with one CTA (320 threads, 5120 channels) or not fit.
     const int row_bytes = threads * kCols * (int)(sizeof(TX) + (y ? 2 : 0));
-    const bool three = 3 * row_bytes <= (threads <= 320 ? 96 : 200) * 1024;
+    const bool three = 3 * row_bytes <= (threads <= 320 ? 96 * 1024 : kRingBytes);
     const int smem = VEC == 8 ? (three ? 3 : 2) * row_bytes : 0;
     // Up to 640 threads a CTA to an SM with 96 registers a thread is faster than two with 64, which spill (6144 channels
     // 572 against 654 us); not for scalar loads, which need the warps (5308 channels 2.77 against 2.03 ms).
@@ -854,8 +856,7 @@ cudaError_t fwd(const bsa_plan& p, const NormP& n, const void* x, const void* y,
     } else if (threads <= 320) {
         kern = k_norm_cta<TX, VEC, 3, 320>;
     }
-    if (smem > kPlainSmem)
-        if (cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) return e;
+    if (cudaError_t e = allow_ring(kern, smem)) return e;
     const Ranges rg{n.rows, (int)std::min<int64_t>(n.rows, (int64_t)p.num_sms * ctas_per_sm(threads, threads <= 320 || roomy ? 102 : 64, smem))};
     kern<<<rg.n, threads, smem, s>>>(n, rg, xi, yi, (TX*)x_out, (__nv_bfloat16*)h);
     return cudaGetLastError();
@@ -875,8 +876,7 @@ template <typename TX, int VEC, int NC, int kThreads, bool kToken, bool kPost, b
 cudaError_t bwd_t(const BwdCall& b) {
     auto kern = k_norm_bwd<TX, VEC, NC, kThreads, kToken, kPost, kRing>;
     const int smem = kRing ? kBwdStages * b.stage : 0;
-    if (smem > kPlainSmem)
-        if (cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) return e;
+    if (cudaError_t e = allow_ring(kern, smem)) return e;
     kern<<<b.rg.n, b.threads, smem, b.s>>>(b.n, b.g, b.rg, (const __nv_bfloat16*)b.dh, (const TX*)b.dx_out,
                                            (const TX*)b.x_out, (const __nv_bfloat16*)b.y, (TX*)b.dx, (__nv_bfloat16*)b.dy);
     return cudaGetLastError();
