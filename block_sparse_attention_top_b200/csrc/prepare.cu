@@ -184,10 +184,7 @@ cudaError_t launch_worklist(const bsa_plan& p, const int32_t* row_ptr, int32_t* 
         key.grank = grank;
         n_bins = groups * ((int)p.nb + 1);
         const size_t smem = (size_t)groups * sizeof(long long);
-        if (smem > 48 * 1024) {
-            cudaError_t e = cudaFuncSetAttribute(k_group_rank, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-            if (e != cudaSuccess) return e;
-        }
+        if (cudaError_t e = allow_smem(k_group_rank, smem, kMaxSchedGroups * sizeof(long long))) return e;
         k_group_rank<<<1, 1024, smem, s>>>(row_ptr, p.rows, key.rows_per_group, groups, grank);
     }
     cudaError_t e = cudaMemsetAsync(hist, 0, (size_t)n_bins * sizeof(int32_t), s);

@@ -905,10 +905,8 @@ cudaError_t launch_route_rows(const bsa_plan& p, const double* scores, double pv
         const unsigned grid = (unsigned)((rows + kBwarpRows - 1) / kBwarpRows);
         const int need = ((nb + 31) / 32) | 1;
         auto run = [&](auto kern) -> cudaError_t {
-            if (smem > 48 * 1024) {
-                cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-                if (e != cudaSuccess) return e;
-            }
+            const size_t most = (size_t)kBwarpRows * bwarp_stride(1024, 2048) * sizeof(unsigned long long);
+            if (cudaError_t e = allow_smem(kern, smem, most)) return e;
             kern<<<grid, 32 * kBwarpRows, smem, s>>>(scores, rows, nb, NB, pval, k_floor, sorted, counts, hr);
             return cudaGetLastError();
         };
@@ -919,11 +917,11 @@ cudaError_t launch_route_rows(const bsa_plan& p, const double* scores, double pv
     if (nbp <= 4096) {
         // exact bucket sort: NB = nbp buckets (a multiple of the block size)
         const int NB = nbp;
-        const size_t smem = (size_t)3 * nb * sizeof(unsigned long long) + (size_t)(nb + 2 * NB) * sizeof(int);
-        if (smem > 48 * 1024) {
-            cudaError_t e = cudaFuncSetAttribute(k_route_bucket, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-            if (e != cudaSuccess) return e;
-        }
+        auto bytes = [](int n, int buckets) {
+            return (size_t)3 * n * sizeof(unsigned long long) + (size_t)(n + 2 * buckets) * sizeof(int);
+        };
+        const size_t smem = bytes(nb, NB);
+        if (cudaError_t e = allow_smem(k_route_bucket, smem, bytes(4096, 4096))) return e;
         k_route_bucket<<<(unsigned)rows, kBucketThreads, smem, s>>>(scores, nb, NB, pval, k_floor, sorted, counts, hr);
         return cudaGetLastError();
     }
@@ -931,10 +929,7 @@ cudaError_t launch_route_rows(const bsa_plan& p, const double* scores, double pv
     const int E = nbp / kCtaSortThreads;
     const size_t smem = (size_t)nbp * sizeof(unsigned long long);
     auto run = [&](auto kern) -> cudaError_t {
-        if (smem > 48 * 1024) {
-            cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-            if (e != cudaSuccess) return e;
-        }
+        if (cudaError_t e = allow_smem(kern, smem, kMaxRouteBlocks * sizeof(unsigned long long))) return e;
         kern<<<(unsigned)rows, kCtaSortThreads, smem, s>>>(scores, nb, pval, k_floor, sorted, counts, hr);
         return cudaGetLastError();
     };

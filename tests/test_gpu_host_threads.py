@@ -42,6 +42,21 @@ extern "C" int norm_gradients(int n, const bsa_plan* p, const bsa_norm_args* wid
     };
     return both(n, [=] { return one(wide, x1, w1, s1); }, [=] { return one(narrow, x2, w2, s2); });
 }
+struct Route {
+    const bsa_plan* p;
+    const void *q, *k;
+    int32_t *rows, *cols;
+    int64_t cap;
+    float* load;
+    int64_t* nnz;
+    void* ws;
+    size_t bytes;
+    void* stream;
+    int operator()() const {
+        return bsa_route(p, q, k, BSA_BF16, 0.5f, 2, rows, cols, cap, load, nnz, ws, bytes, stream);
+    }
+};
+extern "C" int routes(int n, const Route* a, const Route* b) { return both(n, *a, *b); }
 """
 
 
@@ -106,3 +121,31 @@ def test_norm_gradients(bsa, race):
     assert rc == bsa.BSA_OK
     for t, w in zip(got, want):
         assert torch.equal(t, w)
+
+
+class Route(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("p", "q", "k", "rows", "cols")] + [("cap", ctypes.c_int64)] + \
+        [(n, ctypes.c_void_p) for n in ("load", "nnz", "ws")] + [("bytes", ctypes.c_size_t), ("stream", ctypes.c_void_p)]
+
+
+@pytest.mark.parametrize("sizes", [(1009, 1024), (1300, 2000)])
+def test_routing(bsa, race, sizes):
+    calls, checks, keep = [], [], []
+    for nb in sizes:
+        N, d = nb * 64, 64
+        plan = bsa.Plan(1, 1, 1, 1, N, d, 64, bsa.BSA_ORDER_IDENTITY)
+        q, k = rand((1, N, 1, d), nb), rand((1, N, 1, d), nb + 1)
+        want = bsa.route(plan, q, k, 0.5, 2)
+        got, ws, s = [torch.empty_like(t) for t in want], plan.workspace(bsa.BSA_OP_ROUTE), torch.cuda.Stream()
+        calls.append(Route(plan.handle, q.data_ptr(), k.data_ptr(), got[0].data_ptr(), got[1].data_ptr(), got[1].numel(),
+                           got[2].data_ptr(), got[3].data_ptr(), ws.data_ptr(), ws.numel(), s.cuda_stream))
+        checks.append((got, want))
+        keep.append((plan, q, k, ws, s))
+    torch.cuda.synchronize()
+    rc = race.routes(2000, ctypes.byref(calls[0]), ctypes.byref(calls[1]))
+    torch.cuda.synchronize()
+    assert rc == bsa.BSA_OK
+    for got, want in checks:
+        n = int(want[3].item())
+        for a, b in zip((got[0], got[1][:n], got[2], got[3]), (want[0], want[1][:n], want[2], want[3])):
+            assert torch.equal(a, b)
