@@ -389,7 +389,9 @@ k_cross_fwd(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUt
                     m = slot[kTile];
                     ++done[g];
                 }
-                const bool empty = m == -INFINITY;                    // no valid state: zeros
+                // No valid state: zeros.  Told by the sum, which is at least about 1 otherwise; the maximum drops NaN, and
+                // a row of NaN must stay NaN.
+                const bool empty = l == 0.f;
                 const float inv = empty ? 0.f : 1.f / l;
                 if (prm.lse && n < prm.N)
                     prm.lse[((int64_t)it.b * prm.H + it.h) * prm.N + n] =

@@ -85,3 +85,38 @@ def test_norm_modulate_reads_no_gate_and_no_post_weight(bsa, groups, C):
     assert torch.equal(h, h2) and torch.equal(dx, grads.dx)
     for n in par:
         assert torch.equal(out[n], getattr(grads, "d" + n)), n
+
+
+# ------------------------------------------------------------------ cross attention
+
+# rows and states: the tensor-core kernel with one and with several key tiles, and the split kernel
+@pytest.mark.parametrize("N,M", [(200, 40), (200, 300), (3, 40), (1, 700)])
+def test_a_query_row_of_nan_stays_nan(bsa, N, M):
+    """All scores of a row are NaN: so are its output and its lse.  -inf is the sign of a row without valid states."""
+    B, H, d = 2, 2, 64
+    q, k, v = rand((B, N, H, d), 1), rand((B, M, H, d), 2), rand((B, M, H, d), 3)
+    plan = plan_of(bsa, B, N, H, d)
+    for kw in ({}, dict(kv_len=torch.tensor([M - 3, 0], dtype=torch.int32).cuda()),
+               dict(key_mask=(torch.arange(B * M).view(B, M) >= 33).cuda())):
+        o, lse = bsa.cross_attn(plan, q, k, v, return_lse=True, **kw)
+        q2 = q.clone()
+        q2[:, 0, 1, 5] = float("nan")
+        o2, lse2 = bsa.cross_attn(plan, q2, k, v, return_lse=True, **kw)
+        assert bsa.bsa_last_device_error(plan) == bsa.BSA_OK
+        for b in range(B):
+            if "kv_len" in kw and b == 1:
+                assert not o2[b].any() and torch.isneginf(lse2[b]).all()
+                continue
+            assert torch.isnan(o2[b, 0, 1]).all() and torch.isnan(lse2[b, 1, 0])
+            o2[b, 0, 1], lse2[b, 1, 0] = o[b, 0, 1], lse[b, 1, 0]
+        assert torch.equal(o2, o) and torch.equal(lse2, lse)
+
+
+@pytest.mark.parametrize("N,M", [(200, 40), (200, 300), (3, 40), (1, 700)])
+def test_a_query_row_of_scores_minus_infinity_is_empty(bsa, N, M):
+    B, H, d = 1, 2, 64
+    q, k, v = rand((B, N, H, d), 1).abs() + 0.5, rand((B, M, H, d), 2), rand((B, M, H, d), 3)
+    k[:, :, 1] = float("-inf")                                         # the second head: q > 0, so every score is -inf
+    o, lse = bsa.cross_attn(plan_of(bsa, B, N, H, d), q, k, v, return_lse=True)
+    assert not o[:, :, 1].any() and torch.isneginf(lse[:, 1]).all()
+    assert torch.isfinite(o[:, :, 0].float()).all() and torch.isfinite(lse[:, 0]).all()
