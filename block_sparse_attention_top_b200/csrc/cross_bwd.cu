@@ -462,7 +462,8 @@ k_cross_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
             if (n < prm.N) {
                 const int64_t i = ((int64_t)it.b * prm.H + it.h) * prm.N + n;
                 const float l = prm.lse[i];
-                lse2 = l == -INFINITY ? 0.f : l * kLog2e;             // no valid state: every key is masked
+                lse2 = l * kLog2e;
+                if (l == -INFINITY) lse2 = d = 0.f;                   // no valid state: P = 0, and dS = 0 whatever dO holds
             }
             float* rv = row_vals + (nr & 1) * 2 * kTile + r;
             rv[0] = lse2;
@@ -756,7 +757,7 @@ k_cross_dkv(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUt
         DkvWalk w;
         while (ok && w.next_item(prm)) {
             const int j = w.it.kt * kTile + 32 * quad + lane;         // this thread's key
-            const bool on = j < w.it.len && (!prm.keys.key_mask || prm.keys.key_mask[(int64_t)w.it.b * prm.keys.M + j]);
+            const bool on = prm.keys.counts(w.it.b, w.it.len, j);
             for (int s = w.it.beg; s < w.it.end; ++s, ++u) {
                 const int st = u % L::kStages;
                 const uint32_t ts = ts0 + (u & 1) * kKeys, tp = ts - L::colS + L::colDP;
@@ -812,6 +813,8 @@ k_cross_dkv(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUt
                 fence_after();
             }
             const int64_t at = (((int64_t)it.b * prm.keys.M + j) * prm.Hkv + it.hk) * D;
+            // 0 * NaN is NaN: a state that does not count gets its zeros here (of shares: in their sum)
+            const bool on = work && prm.keys.counts(it.b, it.len, j);
 #pragma unroll 1
             for (int c = 0; c < 2 * D / 32; ++c) {
                 const bool is_v = c < D / 32;
@@ -820,10 +823,10 @@ k_cross_dkv(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUt
                 if (work) {
                     tmem_ld32(tl + (is_v ? L::colDV : L::colDK) + col, v);
                     tmem_wait_ld();
-                } else {
+                }
+                if (!on)
 #pragma unroll
                     for (int e = 0; e < 32; ++e) v[e] = 0u;
-                }
                 if (j >= prm.keys.M) continue;
                 if (prm.part) {
                     float4* dst = reinterpret_cast<float4*>(prm.part + ((is_v ? prm.chunks : 0) + it.chunk) * prm.part_stride +
@@ -858,7 +861,8 @@ k_cross_dkv(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUt
     end_cta(tmem);
 }
 
-// dK (scaled) and dV from the shares, in share order; tiles without a valid state are zero.
+// dK (scaled) and dV from the shares, in share order; states that do not count get zeros (no share has written the tiles
+// behind a length).
 __global__ void k_cross_dkv_sum(const DkvP prm, int D) {
     const int64_t i4 = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
     if (i4 * 4 >= prm.part_stride) return;
@@ -866,7 +870,7 @@ __global__ void k_cross_dkv_sum(const DkvP prm, int D) {
     const int64_t row = i4 * 4 / ((int64_t)prm.Hkv * D), b = row / prm.keys.M;
     const int j = (int)(row - b * prm.keys.M);
     float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (j / kTile * kTile < prm.keys.count((int)b)) {
+    if (prm.keys.counts((int)b, prm.keys.count((int)b), j)) {
         const float* src = prm.part + (is_v ? prm.chunks * prm.part_stride : 0) + i4 * 4;
         for (int c = 0; c < prm.chunks; ++c) {
             const float4 v = __ldcs(reinterpret_cast<const float4*>(src + c * prm.part_stride));

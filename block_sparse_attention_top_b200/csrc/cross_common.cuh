@@ -46,6 +46,10 @@ struct Keys {
         const int n = __ldg(kv_len + b);
         return n < 0 ? 0 : (n > M ? M : n);
     }
+    // State j of batch entry b, whose length is len, counts.
+    __device__ __forceinline__ bool counts(int b, int len, int j) const {
+        return j < len && (!key_mask || __ldg(key_mask + (int64_t)b * M + j) != 0);
+    }
     // Warp-collective: bit i of w[i / 32] = key base + i counts (kKeys of them); true if all do.
     __device__ __forceinline__ bool bits(int b, int len, int base, int lane, uint32_t* w) const {
         if (!key_mask) {
@@ -56,7 +60,7 @@ struct Keys {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const int j = base + 32 * i + lane;
-                w[i] = __ballot_sync(0xffffffffu, j < len && __ldg(key_mask + (int64_t)b * M + j) != 0);
+                w[i] = __ballot_sync(0xffffffffu, counts(b, len, j));
             }
         }
         return (w[0] & w[1]) == 0xffffffffu;

@@ -488,7 +488,7 @@ int bsa_cross_attn(const bsa_plan* plan, const void* q, const void* k, const voi
  * head.  q, k, v, M, Hkv, strides, kv_len, key_mask: as in the forward call;
  * o, lse: its outputs; d_o: bf16 [B,N,H,d] dense.  dq [B,N,H,d], dk, dv
  * [B,M,Hkv,d]: bf16, dense; states that do not count get zero gradients, and
- * so do query rows without a valid state.  D comes from the bf16 O; what its
+ * so do query rows without a valid state (whatever d_o holds there).  D comes from the bf16 O; what its
  * rounding makes dS sum to over the states (0 for the exact D) is taken out
  * again, for dK always and for dQ where M <= 64.  P and dS enter the products
  * in bf16, sums are fp32, and the result does not depend on scheduling: the

@@ -120,3 +120,28 @@ def test_a_query_row_of_scores_minus_infinity_is_empty(bsa, N, M):
     o, lse = bsa.cross_attn(plan_of(bsa, B, N, H, d), q, k, v, return_lse=True)
     assert not o[:, :, 1].any() and torch.isneginf(lse[:, 1]).all()
     assert torch.isfinite(o[:, :, 0].float()).all() and torch.isfinite(lse[:, 0]).all()
+
+
+# one key tile, several, and enough rows that the key side's work is split into shares
+@pytest.mark.parametrize("N,M", [(150, 40), (150, 300), (2000, 200)])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_gradients_of_what_does_not_count_are_zero(bsa, bad, N, M):
+    """Query rows without a valid state and states that do not count get zero gradients, whatever d_o holds there."""
+    B, H, d = 3, 2, 64
+    q, k, v, do = rand((B, N, H, d), 1), rand((B, M, H, d), 2), rand((B, M, H, d), 3), rand((B, N, H, d), 4)
+    mask = torch.arange(B * M).view(B, M) % 3 != 1
+    mask[1] = False                                                    # batch entry 1: no state counts
+    mask = mask.cuda()
+    plan = plan_of(bsa, B, N, H, d)
+    o, lse = bsa.cross_attn(plan, q, k, v, key_mask=mask, return_lse=True)
+    want = bsa.cross_attn_backward(plan, do, q, k, v, o, lse, key_mask=mask)
+    do2 = do.clone()
+    do2[1] = bad
+    got = bsa.cross_attn_backward(plan, do2, q, k, v, o, lse, key_mask=mask)
+    assert bsa.bsa_last_device_error(plan) == bsa.BSA_OK
+    for a, b in zip(got, want):
+        assert torch.equal(a, b) and not a[1].any()
+    do2[2, 7] = bad                                                    # a row whose states count: theirs are not finite
+    _, dk, dv = bsa.cross_attn_backward(plan, do2, q, k, v, o, lse, key_mask=mask)
+    assert not dk[~mask].any() and not dv[~mask].any()
+    assert not torch.isfinite(dv[2][mask[2]].float()).all()
