@@ -402,6 +402,7 @@ k_cross_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
             if (g == 0 && n < prm.N) prm.dsum[((int64_t)it.b * prm.H + it.h) * prm.N + n] = -neg_d;
         }
         if (!ok) { ctl->abort = 1; record_error(prm.err, BSA_EDEVICE, -4); }
+        __syncwarp();
         tmem_wait_st();
         tmem_wait_ld();
     } else {
@@ -522,6 +523,7 @@ k_cross_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
         }
         if (!ok) { ctl->abort = 1; record_error(prm.err, BSA_EDEVICE, -5); }
         if (nl > 0) mbar_drain(bar(QD_FULL), (nl - 1) & 1);           // what this warp loaded has landed
+        __syncwarp();
         tmem_wait_ld();
         if (lane == 0) bulk_wait();
     }
@@ -795,6 +797,7 @@ k_cross_dkv(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUt
             }
         }
         if (!ok) { ctl->abort = 1; record_error(prm.err, BSA_EDEVICE, -4); }
+        __syncwarp();
         tmem_wait_st();
         tmem_wait_ld();
     } else if (warp < kMmaWarp) {
@@ -827,8 +830,9 @@ k_cross_dkv(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUt
                 if (!on)
 #pragma unroll
                     for (int e = 0; e < 32; ++e) v[e] = 0u;
-                if (j >= prm.keys.M) continue;
-                if (prm.part) {
+                if (j >= prm.keys.M) {
+                    // nothing to write
+                } else if (prm.part) {
                     float4* dst = reinterpret_cast<float4*>(prm.part + ((is_v ? prm.chunks : 0) + it.chunk) * prm.part_stride +
                                                             at + col);
 #pragma unroll
@@ -848,6 +852,7 @@ k_cross_dkv(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUt
                         dst[e] = w;
                     }
                 }
+                __syncwarp();                                         // lanes past M: the next tmem_ld takes the whole warp
             }
             if (work) {
                 fence_before();
@@ -856,6 +861,7 @@ k_cross_dkv(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUt
             }
         }
         if (!ok) { ctl->abort = 1; record_error(prm.err, BSA_EDEVICE, -5); }
+        __syncwarp();
         tmem_wait_ld();
     }
     end_cta(tmem);

@@ -366,6 +366,7 @@ k_cross_fwd(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUt
             }
         }
         if (!ok) { ctl->abort = 1; record_error(prm.err, BSA_EDEVICE, -4); }
+        __syncwarp();
         tmem_wait_st();
         tmem_wait_ld();
     } else if (warp < kMmaWarp) {
@@ -399,6 +400,7 @@ k_cross_fwd(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUt
 #pragma unroll 1
                 for (int s = 0; s < D / 64; ++s) {
                     uint32_t o[64];
+                    __syncwarp();                                     // tmem_ld takes the whole warp
                     if (it.nt > 0) {
                         tmem_ld32(to + g * 128 + s * 64, o);
                         tmem_ld32(to + g * 128 + s * 64 + 32, o + 32);
@@ -432,6 +434,7 @@ k_cross_fwd(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUt
                 }
             }
         if (!ok) { ctl->abort = 1; record_error(prm.err, BSA_EDEVICE, -5); }
+        __syncwarp();
         tmem_wait_ld();
         if (lane == 0) bulk_wait();
     }
