@@ -795,13 +795,17 @@ def dit_block(plan: Plan, x, mod, qkv, attn_out, cross_q, cross_out, ffn, k_ctx,
 
     x: [B,N,C] bf16 or float32; mod: six float32 [B,groups,C] tensors (shift, scale, gate of the self-attention
     half, then of the feed-forward half).  The host model's projections are callables: qkv(h) -> three [B,N,H,d],
-    attn_out(o) -> y, cross_q(h) -> [B,N,H,d], cross_out(o) -> y, ffn(h) -> y, with h and y bf16 [B,N,C].
+    attn_out(o) -> y, cross_q(h) -> [B,N,H,d], cross_out(o) -> y, ffn(h) -> y, with h and y bf16 [B,N,C].  What qkv
+    returns may be views of one fused projection (the self-attention reads dense tensors: others are copied).
     k_ctx, v_ctx: bf16 [B,M,Hkv,d] projections of the encoder's states; kv_len, key_mask: as for cross_attn;
     cross_weight, cross_bias: affine of the norm before the cross attention.  p, k_floor: as for route.
     Returns the block's output in x's type."""
     t1, s1, g1, t2, s2, g2 = mod
     h = norm_modulate(plan, x, scale=s1, shift=t1, norm=norm, eps=eps)
     q, k, v = qkv(h)
+    for t, name in ((q, "q"), (k, "k"), (v, "v")):
+        _need(plan, t, name, _BF16, (plan.B, plan.N, plan.H, plan.d), dense=False)
+    q, k, v = q.contiguous(), k.contiguous(), v.contiguous()
     row_ptr, col_idx, _, _ = route(plan, q, k, p, k_floor)
     y = attn_out(sparse_attn(plan, q, k, v, row_ptr, col_idx))
     x, h = residual_norm(plan, x, y, gate=g1, weight=cross_weight, bias=cross_bias, norm=norm, eps=eps)

@@ -105,3 +105,16 @@ def test_residual_refuses_branch_and_outputs(bsa):
         bsa.residual_norm(PLAN, X, Y, h_out=X)
     with pytest.raises(ValueError):
         bsa.residual_norm_backward(PLAN, Y, Y, X, Y)                   # dx_out has x's type
+
+
+@pytest.mark.parametrize("bad", [torch.zeros(2, 6, 4, 64), torch.zeros(2, 7, 4, 64, dtype=torch.bfloat16),
+                                 torch.zeros(2, 6, 4, 64, dtype=torch.bfloat16, device="meta"), None])
+@pytest.mark.parametrize("which", range(3))
+def test_dit_block_refuses_what_qkv_returns(bsa, monkeypatch, which, bad):
+    """The self-attention's calls take what they get; dit_block checks it first."""
+    good = torch.zeros(2, 6, 4, 64, dtype=torch.bfloat16)
+    monkeypatch.setattr(bsa, "norm_modulate", lambda *a, **k: Y)
+    monkeypatch.setattr(bsa, "route", lambda *a, **k: pytest.fail("called"))
+    with pytest.raises(ValueError):
+        bsa.dit_block(PLAN, X, [None] * 6, qkv=lambda h: [bad if i == which else good for i in range(3)], attn_out=None,
+                      cross_q=None, cross_out=None, ffn=None, k_ctx=None, v_ctx=None, p=1.0, k_floor=1)

@@ -145,3 +145,45 @@ def test_gradients_of_what_does_not_count_are_zero(bsa, bad, N, M):
     _, dk, dv = bsa.cross_attn_backward(plan, do2, q, k, v, o, lse, key_mask=mask)
     assert not dk[~mask].any() and not dv[~mask].any()
     assert not torch.isfinite(dv[2][mask[2]].float()).all()
+
+
+# ------------------------------------------------------------------------ a whole block
+
+@pytest.mark.parametrize("p", [0.4, 1.0])
+def test_dit_block_is_its_parts(bsa, p):
+    """Bit for bit the calls one after the other, with routing that drops blocks, and with q, k and v as views of one
+    fused projection."""
+    B, H, d, T, Hs, Ws, M, Hkv = 2, 2, 64, 2, 17, 19, 23, 1
+    N, C = T * Hs * Ws, H * d
+    plan = bsa.Plan(B, H, T, Hs, Ws, d, 64)
+    x = rand((B, N, C), 1, torch.float32)
+    mod = [rand((B, T, C), 2 + i, torch.float32, 0.3) for i in range(6)]
+    wqkv, w = rand((C, 3 * C), 10, scale=2 * C ** -0.5), [rand((C, C), 11 + i, scale=C ** -0.5) for i in range(4)]
+    kc, vc = rand((B, M, Hkv, d), 20), rand((B, M, Hkv, d), 21)
+
+    def fused(h):
+        return (h @ wqkv).view(B, N, 3, H, d).unbind(2)
+
+    def heads(t):
+        return t.reshape(B, N, H, d)
+
+    def flat(t):
+        return t.reshape(B, N, C)
+
+    args = dict(attn_out=lambda o: flat(o) @ w[0], cross_q=lambda h: heads(h @ w[1]), cross_out=lambda o: flat(o) @ w[2],
+                ffn=lambda h: h @ w[3], k_ctx=kc, v_ctx=vc, p=p, k_floor=1)
+    got = bsa.dit_block(plan, x, mod, qkv=fused, **args)
+    dense = bsa.dit_block(plan, x, mod, qkv=lambda h: tuple(t.contiguous() for t in fused(h)), **args)
+    t1, s1, g1, t2, s2, g2 = mod
+    h = bsa.norm_modulate(plan, x, scale=s1, shift=t1)
+    q, k, v = (t.contiguous() for t in fused(h))
+    row_ptr, col_idx, _, nnz = bsa.route(plan, q, k, p, 1)
+    assert (int(nnz.item()) < plan.rows * plan.nb) == (p < 1)
+    y = args["attn_out"](bsa.sparse_attn(plan, q, k, v, row_ptr, col_idx))
+    a, h = bsa.residual_norm(plan, x, y, gate=g1)
+    y = args["cross_out"](bsa.cross_attn(plan, args["cross_q"](h), kc, vc))
+    a, h = bsa.residual_norm(plan, a, y, scale=s2, shift=t2)
+    want = bsa.residual_norm(plan, a, args["ffn"](h), gate=g2, norm=bsa.BSA_NORM_NONE)[0]
+    assert bsa.bsa_last_device_error(plan) == bsa.BSA_OK
+    assert torch.equal(dense, want)
+    assert torch.equal(got, want)
