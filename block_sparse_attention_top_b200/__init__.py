@@ -800,15 +800,16 @@ def dit_block(plan: Plan, x, mod, qkv, attn_out, cross_q, cross_out, ffn, k_ctx,
     k_ctx, v_ctx: bf16 [B,M,Hkv,d] projections of the encoder's states; kv_len, key_mask: as for cross_attn;
     cross_weight, cross_bias: affine of the norm before the cross attention.  p, k_floor: as for route.
     Returns the block's output in x's type."""
-    t1, s1, g1, t2, s2, g2 = mod
-    h = norm_modulate(plan, x, scale=s1, shift=t1, norm=norm, eps=eps)
-    q, k, v = qkv(h)
-    for t, name in ((q, "q"), (k, "k"), (v, "v")):
-        _need(plan, t, name, _BF16, (plan.B, plan.N, plan.H, plan.d), dense=False)
-    q, k, v = q.contiguous(), k.contiguous(), v.contiguous()
-    row_ptr, col_idx, _, _ = route(plan, q, k, p, k_floor)
-    y = attn_out(sparse_attn(plan, q, k, v, row_ptr, col_idx))
-    x, h = residual_norm(plan, x, y, gate=g1, weight=cross_weight, bias=cross_bias, norm=norm, eps=eps)
-    y = cross_out(cross_attn(plan, cross_q(h), k_ctx, v_ctx, kv_len=kv_len, key_mask=key_mask))
-    x, h = residual_norm(plan, x, y, scale=s2, shift=t2, norm=norm, eps=eps)
-    return residual_norm(plan, x, ffn(h), gate=g2, norm=BSA_NORM_NONE, eps=eps)[0]
+    with _On(plan, None):                                 # route and sparse_attn launch on the current device
+        t1, s1, g1, t2, s2, g2 = mod
+        h = norm_modulate(plan, x, scale=s1, shift=t1, norm=norm, eps=eps)
+        q, k, v = qkv(h)
+        for t, name in ((q, "q"), (k, "k"), (v, "v")):
+            _need(plan, t, name, _BF16, (plan.B, plan.N, plan.H, plan.d), dense=False)
+        q, k, v = q.contiguous(), k.contiguous(), v.contiguous()
+        row_ptr, col_idx, _, _ = route(plan, q, k, p, k_floor)
+        y = attn_out(sparse_attn(plan, q, k, v, row_ptr, col_idx))
+        x, h = residual_norm(plan, x, y, gate=g1, weight=cross_weight, bias=cross_bias, norm=norm, eps=eps)
+        y = cross_out(cross_attn(plan, cross_q(h), k_ctx, v_ctx, kv_len=kv_len, key_mask=key_mask))
+        x, h = residual_norm(plan, x, y, scale=s2, shift=t2, norm=norm, eps=eps)
+        return residual_norm(plan, x, ffn(h), gate=g2, norm=BSA_NORM_NONE, eps=eps)[0]

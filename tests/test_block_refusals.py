@@ -1,5 +1,6 @@
 """Argument checks of the block operators that need no GPU: the C calls' null and range checks, and the binding's
 type, shape, layout and device checks (on CPU tensors, with a stand-in for the plan)."""
+import contextlib
 import ctypes
 import types
 
@@ -113,8 +114,42 @@ def test_residual_refuses_branch_and_outputs(bsa):
 def test_dit_block_refuses_what_qkv_returns(bsa, monkeypatch, which, bad):
     """The self-attention's calls take what they get; dit_block checks it first."""
     good = torch.zeros(2, 6, 4, 64, dtype=torch.bfloat16)
+    monkeypatch.setattr(bsa, "_On", lambda plan, stream: contextlib.nullcontext())
     monkeypatch.setattr(bsa, "norm_modulate", lambda *a, **k: Y)
     monkeypatch.setattr(bsa, "route", lambda *a, **k: pytest.fail("called"))
     with pytest.raises(ValueError):
         bsa.dit_block(PLAN, X, [None] * 6, qkv=lambda h: [bad if i == which else good for i in range(3)], attn_out=None,
                       cross_q=None, cross_out=None, ffn=None, k_ctx=None, v_ctx=None, p=1.0, k_floor=1)
+
+
+def test_dit_block_runs_on_the_plan_s_device(bsa, monkeypatch):
+    """route and sparse_attn launch on the current device: the block makes that the plan's, around every call."""
+    inside, calls = [], []
+
+    class On:
+        def __init__(self, plan, stream):
+            assert plan is PLAN and stream is None
+
+        def __enter__(self):
+            inside.append(True)
+
+        def __exit__(self, *exc):
+            inside.pop()
+
+    def record(name, value):
+        def call(*a, **k):
+            assert inside, name
+            calls.append(name)
+            return value
+        return call
+
+    q = torch.zeros(2, 6, 4, 64, dtype=torch.bfloat16)
+    monkeypatch.setattr(bsa, "_On", On)
+    for name, value in dict(norm_modulate=Y, route=(None,) * 4, sparse_attn=q, cross_attn=q, residual_norm=(X, Y)).items():
+        monkeypatch.setattr(bsa, name, record(name, value))
+    out = bsa.dit_block(PLAN, X, [None] * 6, qkv=record("qkv", (q, q, q)), attn_out=record("attn_out", Y),
+                        cross_q=record("cross_q", q), cross_out=record("cross_out", Y), ffn=record("ffn", Y), k_ctx=q,
+                        v_ctx=q, p=1.0, k_floor=1)
+    assert out is X and not inside
+    assert calls == ["norm_modulate", "qkv", "route", "sparse_attn", "attn_out", "residual_norm", "cross_q", "cross_attn",
+                     "cross_out", "residual_norm", "ffn", "residual_norm"]
