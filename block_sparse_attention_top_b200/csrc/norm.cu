@@ -819,7 +819,7 @@ int ctas_per_sm(int threads, int regs, int smem) {
 
 // The gradient's CTAs (its workspace depends on them): as many as fit, 8 rows at least to each.
 int bwd_threads(int C) { return ((C + bwd_cols(C) - 1) / bwd_cols(C) + 31) / 32 * 32; }
-// bytes of a ring stage, 0: no ring (rows off the 16-byte grid, or too long)
+// bytes of a ring stage, 0: no ring (rows off the 16-byte grid; more than 8192 channels, 5632 in fp32)
 int bwd_stage_bytes(const bsa_norm_args& a) {
     const int bytes = bwd_threads(a.C) * bwd_cols(a.C) * (2 * (a.dtype == BSA_BF16 ? 2 : 4) + 4);
     return a.C % 8 == 0 && bwd_cols(a.C) == 8 && kBwdStages * bytes <= kRingBytes ? bytes : 0;
@@ -841,18 +841,20 @@ cudaError_t fwd(const bsa_plan& p, const NormP& n, const void* x, const void* y,
         return cudaGetLastError();
     }
     const int threads = row_threads(n.C);
-    // A ring of three rows, of two where three would leave an SM with one CTA (320 threads, 5120 channels) or not fit.
+    // A ring of three rows, of two where three do not fit: fp32 rows with a branch of more than 704 threads (11 264 channels).
     const int row_bytes = threads * kCols * (int)(sizeof(TX) + (y ? 2 : 0));
-    const bool three = 3 * row_bytes <= (threads <= 320 ? 96 * 1024 : kRingBytes);
+    const bool three = 3 * row_bytes <= kRingBytes;
     const int smem = VEC == 8 ? (three ? 3 : 2) * row_bytes : 0;
     // Up to 640 threads a CTA to an SM with 96 registers a thread is faster than two with 64, which spill (6144 channels
     // 572 against 654 us); not for scalar loads, which need the warps (5308 channels 2.77 against 2.03 ms).
     const bool roomy = VEC == 8 && threads <= 640;
     auto kern = k_norm_cta<TX, VEC, 3, 1024>;
     if constexpr (VEC == 8) {
-        if (threads <= 320) kern = three ? k_norm_cta<TX, VEC, 3, 320> : k_norm_cta<TX, VEC, 2, 320>;
+        static_assert(3 * 640 * kCols * (sizeof(TX) + 2) <= kRingBytes, "up to 640 threads have three rows");
+        if (threads <= 320) kern = k_norm_cta<TX, VEC, 3, 320>;
         else if (roomy) kern = k_norm_cta<TX, VEC, 3, 640>;
-        else if (!three) kern = k_norm_cta<TX, VEC, 2, 1024>;
+        if constexpr (sizeof(TX) == 4)
+            if (!three) kern = k_norm_cta<TX, VEC, 2, 1024>;
     } else if (threads <= 320) {
         kern = k_norm_cta<TX, VEC, 3, 320>;
     }
@@ -896,7 +898,8 @@ cudaError_t bwd(const BwdCall& b) {
     }
     if (bwd_cols(b.n.C) == 16)
         return b.n.C % 8 == 0 ? bwd_opts<TX, 8, 16, 1024, false>(b) : bwd_opts<TX, 1, 16, 1024, false>(b);
-    if (b.n.C % 8 == 0) return bwd_opts<TX, 8, 8, 1024, false>(b);
+    if constexpr (sizeof(TX) == 4)                       // (a bf16 row of up to 8192 channels always has a ring)
+        if (b.n.C % 8 == 0) return bwd_opts<TX, 8, 8, 1024, false>(b);
     return b.threads <= 512 ? bwd_opts<TX, 1, 8, 512, false>(b) : bwd_opts<TX, 1, 8, 1024, false>(b);
 }
 

@@ -4,6 +4,8 @@ import ctypes
 import pytest
 import torch
 
+from test_gpu_block import ALL, check_boundary, check_boundary_grad, f64, norm_case, residual_both
+
 pytestmark = pytest.mark.gpu
 
 
@@ -187,3 +189,16 @@ def test_dit_block_is_its_parts(bsa, p):
     assert bsa.bsa_last_device_error(plan) == bsa.BSA_OK
     assert torch.equal(dense, want)
     assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("stream", ["bf16", "f32"])
+@pytest.mark.parametrize("C", [5128, 5632, 5640, 8192, 8200, 10240, 10248, 11264, 11272, 5121, 8193, 10241])
+def test_norms_on_both_sides_of_each_variant_s_widths(bsa, C, stream):
+    """The widths at which the launch takes another kernel (threads, rows in the ring, no ring), in both directions."""
+    for groups in ("frame", "token"):
+        case = norm_case(bsa, 1, 2, 7, C, groups, stream, "layer", "rms", ALL, seed=C, res_scale=0.75)
+        residual_both(bsa, case, seed=C)
+    plan, x, t, kw, opt, store, F = norm_case(bsa, 1, 2, 7, C, "frame", stream, "rms", None, ALL, seed=C, residual=False)
+    h, dh = bsa.norm_modulate(plan, x, **t, **kw), rand(x.shape, C + 1)
+    check_boundary(None, h, f64(x), t, opt, store)
+    check_boundary_grad(bsa.norm_modulate_backward(plan, dh, x, **t, **kw), f64(x), f64(dh), None, t, opt, F, store)
