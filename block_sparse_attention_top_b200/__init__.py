@@ -26,12 +26,16 @@ same plan; `dit_block` runs a whole block:
     h = bsa.norm_modulate(plan, x, scale=s1, shift=t1)                 # x: [B, N, C] bf16 or float32
     x, h = bsa.residual_norm(plan, x, y, gate=g1, scale=s2, shift=t2)  # x + g1 y, then its norm
     # gradients: cross_attn_backward, norm_modulate_backward, residual_norm_backward
+
+None of the calls records an autograd graph: a model that trains through them calls the gradients in the backward of
+a torch.autograd.Function of its own.  The operators above warn where an input requires a gradient that would be lost.
 """
 from __future__ import annotations
 
 import collections
 import ctypes
 import os
+import warnings
 
 import torch
 
@@ -621,6 +625,19 @@ def _need(plan, t, name, dtypes, shape, dense=True):
     raise ValueError(f"{name} must be contiguous")
 
 
+_records = torch.is_grad_enabled
+
+
+def _lost_gradient(name):
+    """An input requires a gradient, and autograd will take the call's result for a constant."""
+    warnings.warn(f"{name} records no autograd graph, and an input requires a gradient: call it in a "
+                  f"torch.autograd.Function whose backward calls {name}_backward, or under torch.no_grad()", stacklevel=3)
+
+
+def _learns(t):
+    return t is not None and t.requires_grad
+
+
 def _workspace(plan, need, workspace):
     if workspace is None:
         return torch.empty(need, dtype=torch.uint8, device=plan.device) if need else None
@@ -639,14 +656,15 @@ def _cross_inputs(plan, q, k, v, kv_len, key_mask):
     M, Hkv = k.shape[1], k.shape[2]
     _need(plan, k, "k", _BF16, (plan.B, M, Hkv, plan.d), dense=False)
     _need(plan, v, "v", _BF16, (plan.B, M, Hkv, plan.d), dense=False)
-    for t, name in ((q, "q"), (k, "k"), (v, "v")):
-        if t.stride(3) != 1:
-            raise ValueError(f"the channels of {name} must be contiguous")
+    sq, sk, sv = q.stride(), k.stride(), v.stride()
+    if sq[3] != 1 or sk[3] != 1 or sv[3] != 1:
+        name = "q" if sq[3] != 1 else "k" if sk[3] != 1 else "v"
+        raise ValueError(f"the channels of {name} must be contiguous")
     if kv_len is not None:
         _need(plan, kv_len, "kv_len", (torch.int32,), (plan.B,))
     if key_mask is not None:
         _need(plan, key_mask, "key_mask", (torch.bool, torch.uint8), (plan.B, M))
-    return M, Hkv, _I64x9(*q.stride()[:3], *k.stride()[:3], *v.stride()[:3])
+    return M, Hkv, _I64x9(*sq[:3], *sk[:3], *sv[:3])
 
 
 def cross_attn(plan: Plan, q, k, v, kv_len=None, key_mask=None, return_lse=False, workspace=None, out=None,
@@ -657,6 +675,8 @@ def cross_attn(plan: Plan, q, k, v, kv_len=None, key_mask=None, return_lse=False
     contiguous, other strides multiples of 8 elements).  kv_len: int32 [B] on the device, key_mask: bool
     [B,M]; a state counts when both say so.  Returns o bf16 [B,N,H,d], or (o, lse float32 [B,H,N])."""
     M, Hkv, strides = _cross_inputs(plan, q, k, v, kv_len, key_mask)
+    if _records() and (q.requires_grad or k.requires_grad or v.requires_grad):
+        _lost_gradient("cross_attn")
     if out is not None:
         _need(plan, out, "out", _BF16, q.shape)
     with _On(plan, stream) as s:
@@ -699,12 +719,18 @@ def _norm_inputs(plan, x, gate, scale, shift, weight, bias, post_weight, norm, p
             raise ValueError("gate, scale and shift must be [B, groups, C]")
         groups = first.shape[1]
         shape = (plan.B, groups, C)
-        for t, name in ((gate, "gate"), (scale, "scale"), (shift, "shift")):
-            if t is not None:
-                _need(plan, t, name, _F32, shape)
-    for t, name in ((weight, "weight"), (bias, "bias"), (post_weight, "post_weight")):
-        if t is not None:
-            _need(plan, t, name, _F32, (C,))
+        if gate is not None:
+            _need(plan, gate, "gate", _F32, shape)
+        if scale is not None:
+            _need(plan, scale, "scale", _F32, shape)
+        if shift is not None:
+            _need(plan, shift, "shift", _F32, shape)
+    if weight is not None:
+        _need(plan, weight, "weight", _F32, (C,))
+    if bias is not None:
+        _need(plan, bias, "bias", _F32, (C,))
+    if post_weight is not None:
+        _need(plan, post_weight, "post_weight", _F32, (C,))
     return NormArgs(C, groups, BSA_BF16 if x.dtype == torch.bfloat16 else BSA_F32, norm, post_norm, eps, res_scale,
                     _ptr(gate), _ptr(scale), _ptr(shift), _ptr(weight), _ptr(bias), _ptr(post_weight))
 
@@ -714,6 +740,8 @@ def norm_modulate(plan: Plan, x, scale=None, shift=None, weight=None, bias=None,
     """h = (norm(x) * weight + bias) * (1 + scale) + shift in bf16 (bsa_norm_modulate).  x: bf16 or float32
     [B,N,C]; scale, shift: float32 [B,groups,C], token n in group n // (N / groups); weight, bias: float32 [C]."""
     a = _norm_inputs(plan, x, None, scale, shift, weight, bias, None, norm, BSA_NORM_NONE, 1.0, eps)
+    if _records() and (x.requires_grad or _learns(scale) or _learns(shift) or _learns(weight) or _learns(bias)):
+        _lost_gradient("norm_modulate")
     if out is not None:
         _need(plan, out, "out", _BF16, x.shape)
     with _On(plan, stream) as s:
@@ -730,6 +758,9 @@ def residual_norm(plan: Plan, x, y, gate=None, scale=None, shift=None, weight=No
     norm_modulate.  norm=BSA_NORM_NONE: no h.  x_out may be x, h_out may be y.  Returns (x_out, h or None)."""
     a = _norm_inputs(plan, x, gate, scale, shift, weight, bias, post_weight, norm, post_norm, res_scale, eps)
     _need(plan, y, "y", _BF16, x.shape)
+    if _records() and (x.requires_grad or y.requires_grad or any(
+            map(_learns, (gate, scale, shift, weight, bias, post_weight)))):
+        _lost_gradient("residual_norm")
     if x_out is not None:
         _need(plan, x_out, "x_out", (x.dtype,), x.shape)
     if h_out is not None:

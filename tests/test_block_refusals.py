@@ -3,6 +3,7 @@ type, shape, layout and device checks (on CPU tensors, with a stand-in for the p
 import contextlib
 import ctypes
 import types
+import warnings
 
 import pytest
 import torch
@@ -153,3 +154,35 @@ def test_dit_block_runs_on_the_plan_s_device(bsa, monkeypatch):
     assert out is X and not inside
     assert calls == ["norm_modulate", "qkv", "route", "sparse_attn", "attn_out", "residual_norm", "cross_q", "cross_attn",
                      "cross_out", "residual_norm", "ffn", "residual_norm"]
+
+
+class Reached(Exception):
+    """The checks are over: the call would launch."""
+
+
+CALLS = [
+    ("cross_attn", _qkv(), ()), ("norm_modulate", dict(x=X), ("scale", "shift", "weight", "bias")),
+    ("residual_norm", dict(x=X, y=Y), ("gate", "scale", "shift", "weight", "bias", "post_weight")),
+]
+
+
+@pytest.mark.parametrize("name,inputs,params", CALLS)
+def test_a_lost_gradient_is_said(bsa, monkeypatch, name, inputs, params):
+    def on(plan, stream):
+        raise Reached
+
+    def call(**over):
+        with pytest.raises(Reached):
+            getattr(bsa, name)(PLAN, **{**inputs, **over})
+
+    monkeypatch.setattr(bsa, "_On", on)
+    given = {**inputs, **{n: torch.zeros(*((24,) if "weight" in n or n == "bias" else (2, 1, 24))) for n in params}}
+    for which, t in given.items():
+        t = t.clone().requires_grad_()
+        with pytest.warns(UserWarning, match=f"{name}_backward"):
+            call(**{which: t})
+        with warnings.catch_warnings():
+            warnings.simplefilter("error")
+            call(**{which: t.detach()})
+            with torch.no_grad():
+                call(**{which: t})
