@@ -4,7 +4,9 @@ import ctypes
 import pytest
 import torch
 
-from test_gpu_block import ALL, check_boundary, check_boundary_grad, f64, norm_case, residual_both
+from oracle import block as ob
+from test_gpu_block import (ALL, check_boundary, check_boundary_grad, check_cross, check_cross_grad, f64, norm_case,
+                            residual_both)
 
 pytestmark = pytest.mark.gpu
 
@@ -202,3 +204,152 @@ def test_norms_on_both_sides_of_each_variant_s_widths(bsa, C, stream):
     h, dh = bsa.norm_modulate(plan, x, **t, **kw), rand(x.shape, C + 1)
     check_boundary(None, h, f64(x), t, opt, store)
     check_boundary_grad(bsa.norm_modulate_backward(plan, dh, x, **t, **kw), f64(x), f64(dh), None, t, opt, F, store)
+
+
+# ------------------------------------------------------------------------ large and many
+
+def gpu_rand(shape, seed, dtype=torch.bfloat16):
+    return torch.randn(*shape, generator=torch.Generator("cuda").manual_seed(seed), dtype=dtype, device="cuda")
+
+
+def test_cross_attention_of_queries_past_32_bits(bsa):
+    """q, o, d_o and dq of more than 2^31 elements: the last rows against a call on those rows alone."""
+    H, d, M, n = 16, 128, 70, 384
+    N = 2 ** 31 // (H * d) + 3 * 128 + 5
+    q, do = gpu_rand((1, N, H, d), 1), gpu_rand((1, N, H, d), 2)
+    k, v = gpu_rand((1, M, H, d), 3), gpu_rand((1, M, H, d), 4)
+    plan, tail = plan_of(bsa, 1, N, H, d), plan_of(bsa, 1, n, H, d)
+    o, lse = bsa.cross_attn(plan, q, k, v, return_lse=True)
+    assert bsa.bsa_last_device_error(plan) == bsa.BSA_OK
+    q1, do1 = q[:, -n:].contiguous(), do[:, -n:].contiguous()
+    o1, lse1 = bsa.cross_attn(tail, q1, k, v, return_lse=True)
+    assert torch.equal(o[:, -n:], o1) and torch.equal(lse[:, :, -n:], lse1)
+    # only the last rows have a gradient: theirs is dq, and all of dk and dv
+    do[:, :-n] = 0
+    dq, dk, dv = bsa.cross_attn_backward(plan, do, q, k, v, o, lse)
+    assert bsa.bsa_last_device_error(plan) == bsa.BSA_OK
+    dq1, dk1, dv1 = bsa.cross_attn_backward(tail, do1, q1, k, v, o1, lse1)
+    assert torch.equal(dq[:, -n:], dq1) and not dq[:, :-n].any()
+    # The same sums in other shares: two roundings to bf16 (2^-8 each), and fp32 sums of n terms whose absolute values
+    # add up to about 5 (dv: sum P |do|; dk: sum |dS| |q| / sqrt(d)) and nowhere to 40: n 2^-24 40 < 1e-3.
+    for a, b in ((dk, dk1), (dv, dv1)):
+        assert ((a - b).float().abs() <= 2 ** -7 * b.float().abs() + 1e-3).all()
+
+
+@pytest.mark.parametrize("N", [1, 130])
+def test_cross_attention_of_states_past_32_bits(bsa, N):
+    """k and v of more than 2^31 elements; only the last states count."""
+    B, H, d, n = 2, 8, 128, 300
+    M = 2 ** 30 // (H * d) + 77
+    k, v = gpu_rand((B, M, H, d), 1), gpu_rand((B, M, H, d), 2)
+    q = gpu_rand((B, N, H, d), 3)
+    mask = torch.zeros(B, M, dtype=torch.bool, device="cuda")
+    mask[:, -n:] = True
+    plan = plan_of(bsa, B, N, H, d)
+    o, lse = bsa.cross_attn(plan, q, k, v, key_mask=mask, return_lse=True)
+    assert bsa.bsa_last_device_error(plan) == bsa.BSA_OK
+    check_cross(o, lse, q, k[:, -n:], v[:, -n:], ob.valid_states(B, n))
+
+
+def test_norms_past_32_bits(bsa):
+    """Streams of more than 2^31 elements: the last rows against a call on those rows alone."""
+    C, n, G = 4096, 64, 5
+    N = G * (2 ** 31 // C // G + 40)
+    x, y = gpu_rand((1, N, C), 1), gpu_rand((1, N, C), 2)
+    par = {name: gpu_rand((1, G, C), 3 + i, torch.float32) for i, name in enumerate(("gate", "scale", "shift"))}
+    last = {name: t[:, -1:].contiguous() for name, t in par.items()}
+    plan, tail = plan_of(bsa, 1, N, 1, 64), plan_of(bsa, 1, n, 1, 64)
+    xo, h = bsa.residual_norm(plan, x, y, **par)
+    x1, y1 = x[:, -n:].contiguous(), y[:, -n:].contiguous()
+    xo1, h1 = bsa.residual_norm(tail, x1, y1, **last)
+    assert torch.equal(xo[:, -n:], xo1) and torch.equal(h[:, -n:], h1)
+    del x
+    g = bsa.residual_norm_backward(plan, h, None, xo, y, **par)
+    g1 = bsa.residual_norm_backward(tail, h1, None, xo1, y1, **last)
+    assert torch.equal(g.dx[:, -n:], g1.dx) and torch.equal(g.dy[:, -n:], g1.dy)
+
+
+def test_cross_attention_of_more_heads_than_a_grid_s_third_extent(bsa):
+    """Few rows and 66 000 key heads: not the split kernel's call."""
+    B, M, d = 66000, 3, 64
+    q, k, v, do = (gpu_rand((B, n, 1, d), i) for i, n in enumerate((1, M, M, 1)))
+    lens = (torch.arange(B, device="cuda") % (M + 1)).int()
+    plan = plan_of(bsa, B, 1, 1, d)
+    o, lse = bsa.cross_attn(plan, q, k, v, kv_len=lens, return_lse=True)
+    grads = bsa.cross_attn_backward(plan, do, q, k, v, o, lse, kv_len=lens)
+    assert bsa.bsa_last_device_error(plan) == bsa.BSA_OK
+    on = ob.valid_states(B, M, lens.cpu().numpy())
+    check_cross(o, lse, q, k, v, on)
+    check_cross_grad(grads, q, k, v, on, do)
+
+
+# ------------------------------------------------------------------------ streams and graphs
+
+def test_streams_by_object_and_by_handle(bsa):
+    """stream= takes torch's streams and raw handles, the default stream's 0 among them."""
+    B, N, H, M, d, C = 1, 300, 2, 100, 64, 136
+    plan = plan_of(bsa, B, N, H, d)
+    q, k, v, do = (rand((B, n, H, d), i) for i, n in enumerate((N, M, M, N)))
+    x, y = rand((B, N, C), 7), rand((B, N, C), 8)
+
+    def step(s):
+        o, lse = bsa.cross_attn(plan, q, k, v, return_lse=True, stream=s)
+        xo, h = bsa.residual_norm(plan, x, y, stream=s)
+        return (o, lse, *bsa.cross_attn_backward(plan, do, q, k, v, o, lse, stream=s), xo, h,
+                *bsa.residual_norm_backward(plan, h, xo, xo, y, stream=s)[:2])
+
+    want = step(None)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    for stream in (s, s.cuda_stream, torch.cuda.default_stream(), 0):
+        got = step(stream)
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
+
+
+def test_one_plan_on_two_streams_at_once(bsa):
+    B, N, H, M, d = 2, 900, 3, 260, 128
+    plan = plan_of(bsa, B, N, H, d)
+    q, k, v, do = (rand((B, n, H, d), i) for i, n in enumerate((N, M, M, N)))
+    mask = (torch.arange(B * M).view(B, M) % 5 != 0).cuda()
+
+    def step(s=None, **kw):
+        o, lse = bsa.cross_attn(plan, q, k, v, return_lse=True, stream=s, **kw)
+        return (o, lse, *bsa.cross_attn_backward(plan, do, q, k, v, o, lse, stream=s, **kw))
+
+    want = step(), step(key_mask=mask)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [(i, step(streams[i], **(dict(key_mask=mask) if i else {}))) for _ in range(10) for i in range(2)]
+    torch.cuda.synchronize()
+    assert bsa.bsa_last_device_error(plan) == bsa.BSA_OK
+    for i, out in got:
+        for a, b in zip(out, want[i]):
+            assert torch.equal(a, b)
+
+
+def test_captured_boundary_without_h(bsa):
+    """A group per token and no h, captured: the zeros of dscale and dshift are part of the graph."""
+    B, N, C = 2, 40, 264
+    plan = plan_of(bsa, B, N, 1, 64)
+    x, y, dxo = rand((B, N, C), 1), rand((B, N, C), 2), rand((B, N, C), 3)
+    par = {n: rand((B, N, C), 4 + i, torch.float32) for i, n in enumerate(("gate", "scale", "shift"))}
+
+    def step():
+        return bsa.residual_norm_backward(plan, None, dxo, x, y, norm=bsa.BSA_NORM_NONE, **par)
+
+    step()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = step()
+    for seed in (11, 12):
+        dxo.copy_(rand(dxo.shape, seed))
+        for t in out:
+            if t is not None:
+                t.fill_(float("nan"))
+        g.replay()
+        for a, b in zip(out, step()):
+            assert (a is None) == (b is None) and (a is None or torch.equal(a, b))
+        assert not out.dscale.any() and not out.dshift.any()
