@@ -23,12 +23,15 @@
 // O_g is rescaled only when the maximum grows by more than 2^8; the softmax
 // warp then waits for PV(t-1).
 //
-// Bound by the exponentials (one MUFU result a score; a share of them as
-// polynomials on the FMA pipe cost 7 % more time) and the hand-offs around
-// them.  Measured: 75 600 tokens, 40 heads of 128, 512 states 0.92 ms,
-// 859 TFLOP/s, 52 % of a bf16 GEMM's rate (the simple fp32 kernel that this
-// one replaced took 129 ms); 32 760 tokens, 12 heads, 257 states 90 us.  Code
-// size counts: each role is one loop body, not one per tile or parity.
+// Bound by the hand-offs between the softmax warps and the tensor cores: a
+// step of 64 keys of both query tiles takes about 2 700 cycles (1.44 us),
+// where its products take 1 280 and its exponentials 1 024 (one MUFU result a
+// score; a share of them as polynomials on the FMA pipe cost 7 % more time).
+// Measured, over several boxes: 75 600 tokens, 40 heads of 128, 512 states
+// 0.92-0.96 ms, 823-861 TFLOP/s, 50-52 % of a bf16 GEMM's rate (the simple
+// fp32 kernel that this one replaced took 129 ms); 32 760 tokens, 12 heads,
+// 257 states 91-94 us.  Code size counts: each role is one loop body, not one
+// per tile or parity.
 //
 // Waits are bounded as in attn_pp.cu.
 #include <algorithm>

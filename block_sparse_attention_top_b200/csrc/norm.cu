@@ -142,8 +142,8 @@ template <int n>
 __device__ __forceinline__ void fetch_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(n) : "memory"); }
 
 // Rows off the 16-byte grid do not come through a ring: their 128-byte lines are brought to L2 two rows ahead, a line to a
-// thread (1219 channels, sandwich: 250 -> 241 us; in the backward kernel it cost 3 %).  (A
-// thread holds at most 64 bytes of the row.)
+// thread (32 760 fp32 rows of 1219 channels, norms on both sides: 251 -> 242 us; in the backward kernel it cost 3 % at
+// 2958 such rows).  (A thread holds at most 64 bytes of the row.)
 template <typename T>
 __device__ __forceinline__ void prefetch_row(const T* p, int C) {
     if (threadIdx.x * 128 < C * sizeof(T))
@@ -845,8 +845,10 @@ cudaError_t fwd(const bsa_plan& p, const NormP& n, const void* x, const void* y,
     const int row_bytes = threads * kCols * (int)(sizeof(TX) + (y ? 2 : 0));
     const bool three = 3 * row_bytes <= kRingBytes;
     const int smem = VEC == 8 ? (three ? 3 : 2) * row_bytes : 0;
-    // Up to 640 threads a CTA to an SM with 96 registers a thread is faster than two with 64, which spill (6144 channels
-    // 572 against 654 us); not for scalar loads, which need the warps (5308 channels 2.77 against 2.03 ms).
+    // Up to 640 threads a CTA to an SM with 96 registers a thread is faster than two with 64, which spill (50 400 bf16 rows
+    // of 6144 channels 573 against 657 us, of 8192 654 against 869; fp32 rows of 8192 1176 against 1580).  Scalar loads
+    // keep the two CTAs for their warps; since their lines are prefetched it makes little difference (5308 channels,
+    // 75 600 bf16 rows 2.98 ms against 3.01 with one; 25 200 fp32 rows 1.01 against 0.93).
     const bool roomy = VEC == 8 && threads <= 640;
     auto kern = k_norm_cta<TX, VEC, 3, 1024>;
     if constexpr (VEC == 8) {

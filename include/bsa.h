@@ -448,7 +448,11 @@ int bsa_attn_run_simt(const bsa_plan* plan, const int32_t* row_ptr, const int32_
  * self-attention they stand next to (its B, N, H, head_dim, device, error
  * word and wait limit; its block size and token order play no part, raster
  * order in and out).  The plan's device must be current (BSA_EINVAL).
- * Device arrays are 16-byte aligned; kv_len and lse 4, key_mask 1.
+ * Device arrays are 16-byte aligned; kv_len and lse 4, key_mask 1.  Outputs
+ * and workspace overlap neither one another nor an input, but where a call
+ * says so.  Calls of these operators may overlap on several streams and come
+ * from several host threads, with one plan too, each with a workspace of its
+ * own; the plan's error word then does not say whose wait ran out.
  * ------------------------------------------------------------------------
  */
 
@@ -463,7 +467,7 @@ int bsa_attn_run_simt(const bsa_plan* plan, const int32_t* row_ptr, const int32_
  * strides: NULL (all three dense), or HOST int64 [9]: the batch, token and
  *   head strides of q, then k, then v, in elements; the d channels of a head
  *   are contiguous.  Multiples of 8, positive wherever the extent exceeds 1,
- *   and of at most 2^39 elements (BSA_EUNSUPPORTED otherwise).
+ *   and below 2^39 elements (BSA_EUNSUPPORTED otherwise).
  * kv_len: device int32 [B] or NULL: state j counts when j < kv_len[b] (values
  *   outside [0, M] act as the nearer bound).  key_mask: device uint8 [B,M] or
  *   NULL: state j counts when its byte is not 0.  Both: a state counts when
