@@ -460,9 +460,9 @@ int bsa_attn_run_simt(const bsa_plan* plan, const int32_t* row_ptr, const int32_
  * Cross attention of the plan's N query tokens to M states of an encoder:
  *   O[b, n, h, :] = sum_j softmax_j(Q[b,n,h,:] . K[b,j,g,:] / sqrt(d)) V[b,j,g,:],
  *   g = h / (H / Hkv), j over the valid states of batch entry b.
- * A query row without any valid state (M = 0, kv_len 0, an all-zero mask, or
- * every score -inf) gives zeros and lse = -inf; one with a NaN score gives NaN
- * for both.
+ * A query row without any valid state (M = 0, kv_len 0, an all-zero mask)
+ * gives zeros and lse = -inf, and so does one whose scores are all -inf; one
+ * with a NaN score gives NaN for both.
  * q: bf16 [B,N,H,d]; k, v: bf16 [B,M,Hkv,d], Hkv divides H.
  * strides: NULL (all three dense), or HOST int64 [9]: the batch, token and
  *   head strides of q, then k, then v, in elements; the d channels of a head

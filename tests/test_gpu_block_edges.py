@@ -206,6 +206,32 @@ def test_norms_on_both_sides_of_each_variant_s_widths(bsa, C, stream):
     check_boundary_grad(bsa.norm_modulate_backward(plan, dh, x, **t, **kw), f64(x), f64(dh), None, t, opt, F, store)
 
 
+
+@pytest.mark.parametrize("C", [200, 1219, 1536, 5632, 8200])
+@pytest.mark.parametrize("groups", ["frame", "token"])
+@pytest.mark.parametrize("post", [None, "layer"])
+def test_residual_norm_gradient_in_place(bsa, post, groups, C):
+    """dx over dx_out and dy over y, as the header allows: the kernel reads the next rows before it writes this one."""
+    plan, x, t, kw, opt, store, F = norm_case(bsa, 2, 3, 50, C, groups, "f32", "layer", post, ALL, seed=C)
+    y, par = t["y"], {n: v for n, v in t.items() if n != "y"}
+    dh, dxo = rand(x.shape, C + 1), rand(x.shape, C + 2, torch.float32)
+    want = bsa.residual_norm_backward(plan, dh, dxo, x, y, **par, **kw)
+    names = ("gate", "scale", "shift", "weight", "bias", "post_weight")
+    a = bsa.NormArgs(C, F, bsa.BSA_F32, kw["norm"], kw["post_norm"], kw["eps"], kw["res_scale"],
+                     *(par[n].data_ptr() for n in names))
+    ws = torch.empty(bsa._lib.bsa_norm_bwd_workspace_size(plan.handle, ctypes.byref(a)), dtype=torch.uint8, device="cuda")
+    out = {n: torch.empty_like(par[n]) for n in names}
+    dx, dy = dxo.clone(), y.clone()
+    rc = bsa._lib.bsa_residual_norm_bwd(plan.handle, ctypes.byref(a), dh.data_ptr(), dx.data_ptr(), x.data_ptr(),
+                                        dy.data_ptr(), dx.data_ptr(), dy.data_ptr(), *(out[n].data_ptr() for n in names),
+                                        ws.data_ptr(), ws.numel(), torch.cuda.current_stream().cuda_stream)
+    assert rc == bsa.BSA_OK
+    torch.cuda.synchronize()
+    assert torch.equal(dx, want.dx) and torch.equal(dy, want.dy)
+    for n in names:
+        assert torch.equal(out[n], getattr(want, "d" + n)), n
+
+
 # ------------------------------------------------------------------------ large and many
 
 def gpu_rand(shape, seed, dtype=torch.bfloat16):
